@@ -19,6 +19,10 @@ namespace {
 
 thread_local char g_msg[512] = "";
 
+}  // namespace
+
+namespace gdn {
+
 int fail(int code, const char *fmt, ...)
 {
     va_list ap;
@@ -35,6 +39,14 @@ int ok()
 }
 
 bool misaligned(const void *p) { return p && (reinterpret_cast<uintptr_t>(p) & 15u) != 0; }
+
+}  // namespace gdn
+
+using gdn::fail;
+using gdn::misaligned;
+using gdn::ok;
+
+namespace {
 
 // Shape / dtype / pointer checks shared by gdn_forward and gdn_rollout.
 int check_common(const void *q, const void *k, const void *v, const float *beta,
@@ -426,6 +438,39 @@ int gdn_forward_fp8(const void *q8, const void *k8, const void *v8, const float 
         return ok();
     } catch (...) {
         return fail(GDN_ERR_CUDA, "internal error in gdn_forward_fp8");
+    }
+}
+
+int gdn_backward(const void *q, const void *k, const void *v, const float *beta, const float *decay,
+                 const float *state_in, const void *dout, const float *dstate_out, void *dq, void *dk_out,
+                 void *dv_out, float *dbeta, float *ddecay, float *dstate_in, int B, int H, int T, int dk,
+                 int dv, int mode, void *stream)
+{
+    try {
+        if (!dout) return fail(GDN_ERR_INVALID_ARG, "dout must be non-NULL");
+        int rc = check_common(q, k, v, beta, decay, state_in, dstate_out, dout, B, H, T, dk, dv, mode, "T");
+        if (rc != GDN_OK) return rc;
+        const void *ptrs[] = {dq, dk_out, dv_out, dbeta, ddecay};
+        for (const void *p : ptrs)
+            if (!p) return fail(GDN_ERR_INVALID_ARG, "dq, dk, dv, dbeta and ddecay must be non-NULL");
+        for (const void *p : ptrs)
+            if (misaligned(p)) return fail(GDN_ERR_MISALIGNED, "a gradient output is not 16-byte aligned");
+        if (misaligned(dstate_in)) return fail(GDN_ERR_MISALIGNED, "dstate_in is not 16-byte aligned");
+        if (mode & GDN_RECURRENT)
+            return fail(GDN_ERR_UNSUPPORTED, "gdn_backward has one form for every size (no GDN_RECURRENT)");
+        gdn::BwdArgs a;
+        a.f = make_args(q, k, v, beta, decay, state_in, nullptr, nullptr, B, H, T, dk, dv, mode);
+        a.dout = dout; a.dstate = dstate_out;
+        a.dq = dq; a.dk = dk_out; a.dv = dv_out;
+        a.dbeta = dbeta; a.ddecay = ddecay; a.dstate_in = dstate_in;
+        cudaError_t err = gdn::launch_backward(a, static_cast<cudaStream_t>(stream));
+        if (err != cudaSuccess) {
+            (void)cudaGetLastError();   // an allocation that failed is reported here alone
+            return fail(GDN_ERR_CUDA, "launch failed: %s", cudaGetErrorString(err));
+        }
+        return ok();
+    } catch (...) {
+        return fail(GDN_ERR_CUDA, "internal error in gdn_backward");
     }
 }
 

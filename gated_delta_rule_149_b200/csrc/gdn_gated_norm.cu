@@ -1,0 +1,290 @@
+// The read-out of the recurrence, normalised per head, scaled and gated, and the gradients of that:
+//     n = o / sqrt(mean(o^2) + eps),   y = n w silu(g)                 per row of dv values
+//     dn = dy w silu(g),   do = r (dn - n mean(dn n)),   r = 1 / sqrt(mean(o^2) + eps)
+//     dg = dy n w (s + g s (1 - s)),   s = sigmoid(g),   dw = sum over rows of dy silu(g) n
+//
+// One pass over the data, which bounds it: o is read head-major as the recurrence writes it, gate and y are
+// token-major as the projections around it take them; a row's 16-byte pieces lie in one group of lanes and its
+// sums are shuffles.  A block keeps one head and walks tokens, so that a thread's columns of the weight, and its
+// sums for dw, stay in registers; the blocks' sums of dw go to a workspace and a second small kernel adds them in
+// a fixed order, so that dw is the same every time.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "gdn_internal.h"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kPer = 8;            // values of a row per lane
+
+struct NormParams {
+    View o, gate, y, dy, dout, dgate;
+    const float *weight;
+    long long w_head;              // elements between two heads' weights (0: shared)
+    float *part;                   // [head][batch][block][dv] sums for dw, or nullptr
+    int T, dv, per_block;          // tokens per block
+    float eps;
+};
+
+// A lane's values of a row: VEC, values 8 l .. 8 l + 7 by 16-byte accesses; otherwise l, l + LPR, ...
+template <bool VEC, int LPR>
+__device__ __forceinline__ int column(int l, int i) { return VEC ? kPer * l + i : l + LPR * i; }
+
+template <bool VEC, int LPR>
+__device__ __forceinline__ void load(const __nv_bfloat16 *p, int l, int dv, float *f)
+{
+    if (VEC) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(p + 8 * l);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            f[2 * i] = __uint_as_float(w[i] << 16);
+            f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) f[i] = l + LPR * i < dv ? __bfloat162float(p[l + LPR * i]) : 0.f;
+    }
+}
+
+template <bool VEC, int LPR>
+__device__ __forceinline__ void load(const float *p, int l, int dv, float *f)
+{
+    if (VEC) {
+        const float4 a = reinterpret_cast<const float4 *>(p + 8 * l)[0], b = reinterpret_cast<const float4 *>(p + 8 * l)[1];
+        f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+        f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) f[i] = l + LPR * i < dv ? p[l + LPR * i] : 0.f;
+    }
+}
+
+template <bool VEC, int LPR>
+__device__ __forceinline__ void store(__nv_bfloat16 *p, int l, int dv, const float *f)
+{
+    if (VEC) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 v = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+        *reinterpret_cast<uint4 *>(p + 8 * l) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (l + LPR * i < dv) p[l + LPR * i] = __float2bfloat16_rn(f[i]);
+    }
+}
+
+template <bool VEC, int LPR>
+__device__ __forceinline__ void store(float *p, int l, int dv, const float *f)
+{
+    if (VEC) {
+        reinterpret_cast<float4 *>(p + 8 * l)[0] = make_float4(f[0], f[1], f[2], f[3]);
+        reinterpret_cast<float4 *>(p + 8 * l)[1] = make_float4(f[4], f[5], f[6], f[7]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+            if (l + LPR * i < dv) p[l + LPR * i] = f[i];
+    }
+}
+
+template <int LPR>
+__device__ __forceinline__ float row_sum(float x)
+{
+#pragma unroll
+    for (int o = LPR / 2; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// 1 / (1 + 2^(-x log2 e)), each step within two units of fp32's last place; 0 and 1 at the far ends
+__device__ __forceinline__ float sigmoid(float x) { return __fdividef(1.f, 1.f + __expf(-x)); }
+
+// Grid (token tiles, heads, batches).
+template <typename T, bool VEC, int LPR, bool GATE, bool BACK>
+__global__ void __launch_bounds__(kThreads) gated_norm_kernel(const __grid_constant__ NormParams p)
+{
+    constexpr int kGroups = kThreads / LPR;
+    const int l = threadIdx.x % LPR, group = threadIdx.x / LPR;
+    const int h = blockIdx.y, b = blockIdx.z;
+    const bool lane_on = column<VEC, LPR>(l, 0) < p.dv;
+    const float inv = 1.f / p.dv;
+    float w[kPer], dw[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+        const int c = column<VEC, LPR>(l, i);
+        w[i] = p.weight && c < p.dv ? p.weight[h * p.w_head + c] : 1.f;
+        dw[i] = 0.f;
+    }
+    const T *o = static_cast<const T *>(p.o.p) + b * p.o.sb + h * p.o.sh;
+    const T *gate = static_cast<const T *>(p.gate.p) + b * p.gate.sb + h * p.gate.sh;
+    const T *dy = static_cast<const T *>(p.dy.p) + b * p.dy.sb + h * p.dy.sh;
+    const long long t0 = (long long)blockIdx.x * p.per_block;
+    const long long end = min(t0 + p.per_block, (long long)p.T);
+    const int rounds = (int)((end - t0 + kGroups - 1) / kGroups);
+#pragma unroll 2
+    for (int k = 0; k < rounds; ++k) {
+        const long long t = t0 + group + (long long)k * kGroups;
+        const bool act = lane_on && t < end;
+        float x[kPer], g[kPer], z[kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) x[i] = g[i] = z[i] = 0.f;
+        if (act) {
+            load<VEC, LPR>(o + t * p.o.st, l, p.dv, x);
+            if (GATE) load<VEC, LPR>(gate + t * p.gate.st, l, p.dv, g);
+            if (BACK) load<VEC, LPR>(dy + t * p.dy.st, l, p.dv, z);
+        }
+        float sq = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sq = fmaf(x[i], x[i], sq);
+        const float r = rsqrtf(fmaf(row_sum<LPR>(sq), inv, p.eps));
+        if (!BACK) {
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                x[i] *= r * w[i];
+                if (GATE) x[i] *= g[i] * sigmoid(g[i]);
+            }
+            if (act) store<VEC, LPR>(const_cast<T *>(static_cast<const T *>(p.y.p)) + b * p.y.sb + h * p.y.sh + t * p.y.st, l, p.dv, x);
+        } else {
+            float dot = 0.f, dg[kPer];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                const float n = x[i] * r;
+                float act_ = 1.f;
+                if (GATE) {
+                    const float s = sigmoid(g[i]);
+                    act_ = g[i] * s;
+                    dg[i] = z[i] * n * w[i] * fmaf(act_, 1.f - s, s);
+                }
+                const float u = z[i] * act_;
+                dw[i] = fmaf(u, n, dw[i]);
+                z[i] = u * w[i];
+                x[i] = n;
+                dot = fmaf(z[i], n, dot);
+            }
+            dot = row_sum<LPR>(dot) * inv;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) x[i] = r * fmaf(-x[i], dot, z[i]);
+            if (act) {
+                store<VEC, LPR>(const_cast<T *>(static_cast<const T *>(p.dout.p)) + b * p.dout.sb + h * p.dout.sh + t * p.dout.st, l, p.dv, x);
+                if (GATE) store<VEC, LPR>(const_cast<T *>(static_cast<const T *>(p.dgate.p)) + b * p.dgate.sb + h * p.dgate.sh + t * p.dgate.st, l, p.dv, dg);
+            }
+        }
+    }
+    if (BACK && p.part) {
+        __shared__ float sum[kThreads * kPer];
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sum[group * LPR * kPer + column<VEC, LPR>(l, i)] = dw[i];
+        __syncthreads();
+        float *out = p.part + (((size_t)h * gridDim.z + b) * gridDim.x + blockIdx.x) * p.dv;
+        for (int c = threadIdx.x; c < p.dv; c += kThreads) {
+            float x = 0.f;
+            for (int q = 0; q < kGroups; ++q) x += sum[q * LPR * kPer + c];
+            out[c] = x;
+        }
+    }
+}
+
+// dw[block y][c] = the sum of n consecutive partial rows: grid (columns / 32, sets), 32 columns x 32 parts of the
+// rows per block
+__global__ void __launch_bounds__(1024) weight_sum_kernel(const float *part, float *dw, int n, int dv)
+{
+    __shared__ float sum[32][33];
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    const float *in = part + (size_t)blockIdx.y * n * dv;
+    float x = 0.f;
+    if (c < dv)
+        for (int i = threadIdx.y; i < n; i += 32) x += in[(size_t)i * dv + c];
+    sum[threadIdx.y][threadIdx.x] = x;
+    __syncthreads();
+    x = sum[threadIdx.x][threadIdx.y];
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    if (threadIdx.x == 0 && blockIdx.x * 32 + threadIdx.y < dv) dw[(size_t)blockIdx.y * dv + blockIdx.x * 32 + threadIdx.y] = x;
+}
+
+bool rows_aligned(const View &v, int esize)
+{
+    const long long per = 16 / esize;
+    return !v.p || ((reinterpret_cast<uintptr_t>(v.p) & 15u) == 0 && v.sb % per == 0 && v.sh % per == 0 && v.st % per == 0);
+}
+
+template <typename T, bool VEC, int LPR>
+cudaError_t run(const GatedNormArgs &a, const NormParams &p, dim3 grid, cudaStream_t stream)
+{
+    if (a.back) {
+        if (a.gate.p) gated_norm_kernel<T, VEC, LPR, true, true><<<grid, kThreads, 0, stream>>>(p);
+        else gated_norm_kernel<T, VEC, LPR, false, true><<<grid, kThreads, 0, stream>>>(p);
+    } else {
+        if (a.gate.p) gated_norm_kernel<T, VEC, LPR, true, false><<<grid, kThreads, 0, stream>>>(p);
+        else gated_norm_kernel<T, VEC, LPR, false, false><<<grid, kThreads, 0, stream>>>(p);
+    }
+    const cudaError_t err = cudaGetLastError();
+    if (err == cudaSuccess) count_launches(1);
+    return err;
+}
+
+template <typename T>
+cudaError_t run_typed(const GatedNormArgs &a, const NormParams &p, bool vec, int lanes, dim3 grid, cudaStream_t stream)
+{
+    if (!vec) return run<T, false, 32>(a, p, grid, stream);
+    switch (lanes) {
+        case 4: return run<T, true, 4>(a, p, grid, stream);
+        case 8: return run<T, true, 8>(a, p, grid, stream);
+        case 16: return run<T, true, 16>(a, p, grid, stream);
+        default: return run<T, true, 32>(a, p, grid, stream);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_gated_norm(const GatedNormArgs &a, cudaStream_t stream)
+{
+    const int esize = a.fp32 ? 4 : 2;
+    bool vec = a.dv % kPer == 0;
+    for (const View *v : {&a.o, &a.gate, &a.y, &a.dy, &a.dout, &a.dgate}) vec = vec && rows_aligned(*v, esize);
+    int lanes = vec ? 4 : 32;
+    while (lanes * kPer < a.dv) lanes *= 2;
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err != cudaSuccess) return err;
+    // tokens per block: whole rounds of the block's groups, as many as leave every SM eight blocks; the backward
+    // pass, whose blocks each end in a sum over their threads, takes up to 64 rounds, the forward pass up to 8
+    const int groups = kThreads / lanes;
+    const long long rows = (long long)a.B * a.H * a.T, want = rows / ((long long)sms * 8 * groups);
+    const int rounds = (int)std::max<long long>(1, std::min<long long>(want, a.back ? 64 : 8));
+    NormParams p;
+    p.o = a.o; p.gate = a.gate; p.y = a.y; p.dy = a.dy; p.dout = a.dout; p.dgate = a.dgate;
+    p.weight = a.weight;
+    p.w_head = a.per_head ? a.dv : 0;
+    p.part = nullptr;
+    p.T = a.T; p.dv = a.dv; p.per_block = rounds * groups; p.eps = a.eps;
+    const int tiles = (int)(((long long)a.T + p.per_block - 1) / p.per_block);
+    const dim3 grid(tiles, a.H, a.B);
+    if (a.back && a.dweight) {
+        err = ws_alloc(reinterpret_cast<void **>(&p.part), (size_t)a.H * a.B * tiles * a.dv * sizeof(float), stream);
+        if (err != cudaSuccess) return err;
+    }
+    err = a.fp32 ? run_typed<float>(a, p, vec, lanes, grid, stream) : run_typed<__nv_bfloat16>(a, p, vec, lanes, grid, stream);
+    if (p.part) {
+        if (err == cudaSuccess) {
+            const int sets = a.per_head ? a.H : 1, n = a.B * tiles * (a.per_head ? 1 : a.H);
+            weight_sum_kernel<<<dim3((a.dv + 31) / 32, sets), dim3(32, 32), 0, stream>>>(p.part, a.dweight, n, a.dv);
+            err = cudaGetLastError();
+            if (err == cudaSuccess) count_launches(1);
+        }
+        const cudaError_t e2 = ws_free(p.part, stream);
+        if (err == cudaSuccess) err = e2;
+    }
+    return err;
+}
+
+}  // namespace gdn

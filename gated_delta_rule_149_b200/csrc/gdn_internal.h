@@ -68,6 +68,57 @@ cudaError_t launch_normalized(const FwdArgs &a, const float *state_z_in, float *
 cudaError_t launch_fp8(const FwdArgs &a, const float *q_scale, const float *k_scale, const float *v_scale,
                        cudaStream_t stream);
 
+// Gradients of one forward/bidi pass (f.o and f.state_out unused).
+struct BwdArgs {
+    FwdArgs f;
+    const void *dout;         // [B,H,T,dv], dtype of q
+    const float *dstate;      // gradient of state_out (its shape), or nullptr for zero
+    void *dq, *dk, *dv;
+    float *dbeta, *ddecay;
+    float *dstate_in;         // [B,H,dk,dv] or nullptr
+};
+cudaError_t launch_backward(const BwdArgs &a, cudaStream_t stream);
+
+// A strided [B,H,T,d] tensor in device memory, d contiguous; strides in elements.
+struct View {
+    const void *p;
+    long long sb, sh, st;
+};
+
+// Rotation of q (and k) by positions of up to three axes, with an optional L2 normalisation of each row
+// before it; back: the transposed maps applied to gradients g (x: the rows before the normalisation).
+struct RotaryArgs {
+    View x[2], g[2], y[2];    // q, k; y is written
+    int n;                    // 1 (q alone) or 2
+    const int *positions;     // [B or 1][T][3], or nullptr: the grid
+    long long pos_sb;         // elements between two batches' positions (0: shared)
+    int B, H, T, d;
+    int axes[3];              // dims of each axis, even, sum d
+    int grid_h, grid_w;
+    long long start;
+    double theta;
+    float eps;
+    bool half, l2, back, fp32;
+};
+cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t stream);
+
+// y = w o / rms(o) silu(gate) per row of dv values, or its gradients.
+struct GatedNormArgs {
+    View o, gate, y, dy, dout, dgate;   // gate.p may be nullptr; forward writes y, backward dout and dgate
+    const float *weight;      // [dv], [H][dv] (per_head) or nullptr
+    float *dweight;           // same shape
+    bool per_head;
+    int B, H, T, dv;
+    float eps;
+    bool back, fp32;
+};
+cudaError_t launch_gated_norm(const GatedNormArgs &a, cudaStream_t stream);
+
+// Records a message for gdn_last_error and returns the code; clears it and returns GDN_OK.
+int fail(int code, const char *fmt, ...);
+int ok();
+bool misaligned(const void *p);
+
 // Scratch memory: stream-ordered allocations from the library's own pool on
 // the current device, which keeps its reservation across synchronisations;
 // ws_release trims it to nothing, ws_reserved reads its size.

@@ -5,6 +5,7 @@ and passes raw pointers and sizes to the library; all computation happens in
 the library's CUDA kernels.  There is no CPU or fallback path: if libgdn.so
 cannot be loaded, calls raise.
 """
+import contextlib
 import ctypes
 import os
 
@@ -27,6 +28,12 @@ class GDNError(RuntimeError):
     def __init__(self, code, msg):
         super().__init__(f"{_STATUS.get(code, code)}: {msg}")
         self.code = code
+
+
+class View(ctypes.Structure):
+    """gdn_view: a strided [B,H,T,d] tensor, d contiguous."""
+    _fields_ = [("data", ctypes.c_void_p), ("stride_b", ctypes.c_longlong), ("stride_h", ctypes.c_longlong),
+                ("stride_t", ctypes.c_longlong)]
 
 
 def lib_path():
@@ -59,6 +66,18 @@ def load_library():
         lib.gdn_forward_normalized.restype = i
         lib.gdn_forward_fp8.argtypes = [vp] * 11 + [i] * 6 + [vp]
         lib.gdn_forward_fp8.restype = i
+        lib.gdn_backward.argtypes = [vp] * 14 + [i] * 6 + [vp]
+        lib.gdn_backward.restype = i
+        view, ll = ctypes.POINTER(View), ctypes.c_longlong
+        tail = [vp, ll] + [i] * 9 + [ll, ctypes.c_double, ctypes.c_float, i, vp]
+        lib.gdn_rotary.argtypes = [view] * 4 + tail
+        lib.gdn_rotary.restype = i
+        lib.gdn_rotary_backward.argtypes = [view] * 6 + tail
+        lib.gdn_rotary_backward.restype = i
+        lib.gdn_gated_norm.argtypes = [view, view, vp, i, view] + [i] * 4 + [ctypes.c_float, i, vp]
+        lib.gdn_gated_norm.restype = i
+        lib.gdn_gated_norm_backward.argtypes = [view] * 3 + [vp, i, view, view, vp] + [i] * 4 + [ctypes.c_float, i, vp]
+        lib.gdn_gated_norm_backward.restype = i
         lib.gdn_rollout.argtypes = [vp] * 9 + [i] * 7 + [vp]
         lib.gdn_rollout.restype = i
         lib.gdn_device_status.argtypes = [vp]
@@ -157,6 +176,55 @@ def gdn_forward(q, k, v, beta, decay, state_in=None, *, bidi=False, recurrent=Fa
                            _ptr(state_out), _ptr(o), B, H, T, dk, dv,
                            _mode(q, bidi, recurrent), _stream_handle(stream, dev)))
     return o, state_out
+
+
+@contextlib.contextmanager
+def _on(device, stream):
+    """Runs a call with its tensors' device current, and its outputs allocated on the stream that writes them."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+        else:
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
+
+
+def gdn_backward(q, k, v, beta, decay, do, state_in=None, dstate=None, *, bidi=False, stream=None):
+    """Gradients of gdn_forward(q, k, v, beta, decay, state_in, bidi=bidi).
+
+    do [B,H,T,dv] (dtype of q) is the gradient of o, dstate that of the returned
+    state (fp32 [B,H,dk,dv], bidi [2,B,H,dk,dv]) or None for zero; the other
+    arguments are the forward call's.  Returns dq, dk, dv (dtype of q), dbeta,
+    ddecay [B,H,T] and dstate_in [B,H,dk,dv] (fp32; also without state_in).
+    dk, dv multiples of 32, <= 128, for both dtypes.
+    """
+    if q.dim() != 4 or v.dim() != 4:
+        raise ValueError(f"q, k, v must be [B,H,T,d], got {tuple(q.shape)} and {tuple(v.shape)}")
+    B, H, T, dk = q.shape
+    dv = v.shape[-1]
+    dev = q.device
+    if dev.type != "cuda":
+        raise ValueError("gdn_backward runs on CUDA tensors only")
+    mode = _mode(q, bidi, False)
+    _expect(q, "q", (B, H, T, dk), q.dtype, dev)
+    _expect(k, "k", (B, H, T, dk), q.dtype, dev)
+    _expect(v, "v", (B, H, T, dv), q.dtype, dev)
+    _expect(do, "do", (B, H, T, dv), q.dtype, dev)
+    _expect(beta, "beta", (B, H, T), torch.float32, dev)
+    _expect(decay, "decay", (B, H, T), torch.float32, dev)
+    if state_in is not None:
+        _expect(state_in, "state_in", (B, H, dk, dv), torch.float32, dev)
+    if dstate is not None:
+        _expect(dstate, "dstate", ((2,) if bidi else ()) + (B, H, dk, dv), torch.float32, dev)
+    lib = load_library()
+    with _on(dev, stream) as handle:
+        dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+        db, da = torch.empty_like(beta), torch.empty_like(decay)
+        ds = torch.empty(B, H, dk, dv, dtype=torch.float32, device=dev)
+        _check(lib.gdn_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(decay), _ptr(state_in), _ptr(do),
+                                _ptr(dstate), _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(db), _ptr(da), _ptr(ds),
+                                B, H, T, dk, dv, mode, handle))
+    return dq, dk_, dv_, db, da, ds
 
 
 def gdn_forward_segmented(q, k, v, beta, decay, state_in=None, *, n_segments=4, o=None,

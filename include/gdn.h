@@ -67,7 +67,9 @@ enum gdn_mode_bits {
     GDN_BIDI = 1,
     GDN_BF16 = 0,
     GDN_FP32 = 2,
-    GDN_RECURRENT = 4
+    GDN_RECURRENT = 4,
+    GDN_ROTARY_HALF = 16,        /* gdn_rotary: pairs (p, p + d/2) instead of (2p, 2p + 1)         */
+    GDN_ROTARY_L2 = 32           /* gdn_rotary: rows are L2-normalised before the rotation         */
 };
 
 enum gdn_status {
@@ -281,6 +283,98 @@ int gdn_forward_fp8(const void *q8, const void *k8, const void *v8,
                     const float *beta, const float *decay,
                     const float *state_in, float *state_out, void *o,
                     int B, int H, int T, int dk, int dv, int mode, void *stream);
+
+/*
+ * gdn_backward -- the gradients of gdn_forward.
+ *
+ * q, k, v, beta, decay, state_in and mode (GDN_CAUSAL or GDN_BIDI, GDN_BF16 or
+ * GDN_FP32) are those of the forward call; dout [B,H,T,dv] (dtype of q) is the
+ * gradient of o and dstate_out that of state_out (same shape: [B,H,dk,dv], bidi
+ * [2,B,H,dk,dv]; NULL: zero).  Written: dq, dk_out [B,H,T,dk], dv_out [B,H,T,dv]
+ * (dtype of q, each rounded once from fp32, also where a bidirectional call sums
+ * two directions), dbeta, ddecay [B,H,T] fp32, and dstate_in [B,H,dk,dv] fp32
+ * unless NULL.  Nothing of the forward call is needed but its inputs: the states
+ * are recomputed.  All arithmetic is of fp32 grade in both dtypes, whatever the
+ * precision of the forward kernel that ran.
+ *
+ * dk, dv: multiples of 32, <= 128, for both dtypes.  beta may be 0.  A decay below
+ * 2^-120 acts as 2^-120 and has the gradient of that value.  Same results on every
+ * call with the same arguments (no atomics).  Workspace (stream-ordered): about
+ * 4 (2 dk dv + 128 dv + 12288) bytes per head, 64-token chunk and direction, heads
+ * in passes of at most 6 GiB (one head at least).
+ * Errors: as gdn_forward; GDN_RECURRENT returns GDN_ERR_UNSUPPORTED.
+ */
+int gdn_backward(const void *q, const void *k, const void *v,
+                 const float *beta, const float *decay, const float *state_in,
+                 const void *dout, const float *dstate_out,
+                 void *dq, void *dk_out, void *dv_out, float *dbeta, float *ddecay,
+                 float *dstate_in, int B, int H, int T, int dk, int dv, int mode, void *stream);
+
+/* A strided [B,H,T,d] tensor in device memory, d contiguous; strides in elements.
+ * [B,T,H,d] memory is {p, T*H*d, d, H*d}; [B,H,T,d] memory is {p, H*T*d, T*d, d}. */
+typedef struct gdn_view {
+    void *data;
+    long long stride_b, stride_h, stride_t;
+} gdn_view;
+
+/*
+ * gdn_rotary -- positions on q and k: each row of d values is (GDN_ROTARY_L2)
+ * divided by sqrt(|x|^2 + eps) and its pairs are rotated by the angles of up to
+ * three axes, time, height and width.  The layout changes on the way: q and k in
+ * the strides of the projection that made them, the outputs in any others
+ * (contiguous [B,H,T,d] is what gdn_forward takes).
+ *
+ * axis_t + axis_h + axis_w = d, each even and >= 0: pair p of the d/2 belongs to
+ * the axis whose range holds it, as its i-th pair, and turns by
+ * position * theta^(-2 i / axis_dim).  Pair p is elements (2p, 2p + 1), or
+ * (p, p + d/2) with GDN_ROTARY_HALF.  Positions: with `positions` (int32
+ * [B or 1][T][3]; pos_stride_b elements between batches, 0 to share one set), its
+ * values, of any sign; with NULL, token t is number start + t of a sequence of
+ * frames of grid_h x grid_w tokens, row by row (a streaming chunk gives the
+ * number of tokens before it as start).
+ *
+ * gdn_rotary_backward takes the gradients dq, dk of the outputs and, with
+ * GDN_ROTARY_L2, the inputs q, k (else NULL), and writes the inputs' gradients.
+ * k and its counterparts may be NULL together (q alone).  d even, 2 .. 256; bf16
+ * or fp32 (GDN_FP32); sizes that are no multiple of 16, or rows off 16-byte
+ * boundaries, take a slower element-wise path.  Outputs must not overlap
+ * anything.  No workspace.
+ * Errors: GDN_ERR_INVALID_ARG for NULL data, sizes or strides out of range, axes
+ * that do not sum to d, start < 0, theta <= 0, eps <= 0 with GDN_ROTARY_L2;
+ * GDN_ERR_UNSUPPORTED for d > 256; GDN_ERR_MISALIGNED for data off its element
+ * size.
+ */
+int gdn_rotary(const gdn_view *q, const gdn_view *k, const gdn_view *q_out, const gdn_view *k_out,
+               const int *positions, long long pos_stride_b, int B, int H, int T, int d,
+               int axis_t, int axis_h, int axis_w, int grid_h, int grid_w, long long start,
+               double theta, float eps, int mode, void *stream);
+int gdn_rotary_backward(const gdn_view *dq, const gdn_view *dk, const gdn_view *q, const gdn_view *k,
+                        const gdn_view *q_grad, const gdn_view *k_grad,
+                        const int *positions, long long pos_stride_b, int B, int H, int T, int d,
+                        int axis_t, int axis_h, int axis_w, int grid_h, int grid_w, long long start,
+                        double theta, float eps, int mode, void *stream);
+
+/*
+ * gdn_gated_norm -- the read-out, normalised per head, scaled and gated:
+ *     y = weight * o / sqrt(mean(o^2) + eps) * gate * sigmoid(gate)
+ * per row of dv values.  o, gate (NULL: no gate) and y are strided; o comes
+ * head-major from gdn_forward, gate and y are token-major in a layer.  weight:
+ * fp32 [dv], or [H][dv] with per_head, or NULL for 1.
+ *
+ * gdn_gated_norm_backward: from dy, the gradients dout of o, dgate (given exactly
+ * when gate is) and dweight (fp32, shape of weight; NULL to skip; the same on every
+ * call with the same arguments).  dv 1 .. 256; bf16 or fp32 (GDN_FP32, the only
+ * mode bit); sizes that are no multiple of 8, or rows off 16-byte boundaries, take
+ * a slower element-wise path.  Outputs must not overlap anything.  Workspace
+ * (stream-ordered, backward with dweight only): 4 dv bytes per block of tokens.
+ * Errors: as gdn_rotary.
+ */
+int gdn_gated_norm(const gdn_view *o, const gdn_view *gate, const float *weight, int per_head,
+                   const gdn_view *y, int B, int H, int T, int dv, float eps, int mode, void *stream);
+int gdn_gated_norm_backward(const gdn_view *dy, const gdn_view *o, const gdn_view *gate,
+                            const float *weight, int per_head, const gdn_view *dout,
+                            const gdn_view *dgate, float *dweight, int B, int H, int T, int dv,
+                            float eps, int mode, void *stream);
 
 /*
  * gdn_device_status -- synchronises `stream` and reports (and clears) the
