@@ -23,10 +23,21 @@
 // The sums are taken as prefix sums along j and then over i, never as differences, so a strong decay
 // loses nothing to cancellation.
 //
-// Kernels: prepare (X, P, N of every chunk, all chunks at once); chains (two serial walks, forward for
-// H0 and W, backward for dH1 and Z, which need nothing of one another and run side by side, each split
-// over 32-column slices of dv, whose columns are independent); gradients (every chunk at once, both
-// scan directions of a tile in one block, so that a bidirectional call's sums are rounded once).
+// Products run on the tensor cores with bf16 operands and fp32 sums, at fp32 grade: an fp32 operand is three bf16
+// terms, x = h + m + l (24 bits of significand), and of the products of terms those of total order under three are
+// taken; a bf16 input is one term and exact.  Two terms would halve the products and leave 3e-6 (rel-L2) in the fp32
+// gradients where three leave 2e-7; only dQ's and dK's products with E and F, whose results are rounded to
+// bf16, take two.
+//
+// Kernels:
+// * prepare (a block per chunk and direction): brings K, Q, V, dO into scan order as term planes in the
+//   layout that the other two load without conversion, forms N and P likewise.
+// * chains (two serial walks, forward for H0 and W, backward for dH1 and Z, which need nothing of one another
+//   and run side by side): the columns of dv are independent, and a warp carries 16 of them through the whole
+//   sequence by itself.  It holds H^T (16 x dk) as accumulator fragments, which are, split into terms, the left
+//   operands of the next product; so the walk's three dependent products pass through registers, no state goes through
+//   shared memory, and the block's barrier only paces the double-buffered operands.
+// * gradients (a block per chunk, both scan directions, so that a bidirectional call's sums are rounded once).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -34,20 +45,44 @@
 #include <cstdint>
 
 #include "gdn_internal.h"
+#include "sm100_ptx.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kC = 64;         // tokens per chunk
-constexpr int kThreads = 256;
-constexpr int kSl = 32;        // dv columns per slice
-constexpr int kLdC = kC + 4;   // row pitch of 64-wide fp32 tiles in shared memory
-constexpr int kLdS = kSl + 4;  // row pitch of 32-wide tiles
+constexpr int kC = 64;             // tokens per chunk
+constexpr int kSlice = 64;         // dv columns per chain block and per V / dO tile
+constexpr int kTri = kC * kC * 2;  // bytes of one term plane of N or P
 
 __device__ __forceinline__ float ldf(const float *p) { return *p; }
 __device__ __forceinline__ float ldf(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void stf(float *p, float x) { *p = x; }
-__device__ __forceinline__ void stf(__nv_bfloat16 *p, float x) { *p = __float2bfloat16_rn(x); }
+__device__ __forceinline__ void st2(float *p, float x, float y) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); }
+__device__ __forceinline__ void st2(__nv_bfloat16 *p, float x, float y)
+{
+    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
+}
+
+// Gates of a chunk in scan order, as prepare leaves them for the other kernels.  a is clamped as in the
+// forward kernels; behind the sequence's end a = 1 and b = 0.  The running sums of log2 a are held in 64 bits: a strong
+// decay brings them to several hundred within a chunk, where 32 bits would leave differences of neighbours 1e-5 off.
+struct Gates {
+    float gam[kC], e[kC], b[kC], a[kC];
+    double G[kC];
+};
+
+// Workspace of one (direction, head, chunk), in bytes.  Tiles are row-major with the 16-byte pieces of a
+// row XOR-ed by row % 8, so that eight rows' pieces of one column lie in eight bank groups.
+template <int DK, int NI>
+struct Unit {
+    static constexpr size_t kKey = (size_t)kC * DK * 2;    // one term plane of K or Q
+    static constexpr size_t gates = 0;
+    static constexpr size_t N = sizeof(Gates);             // three planes [i][j]
+    static constexpr size_t K = N + 3 * kTri;              // NI planes [token][dk]
+    static constexpr size_t Q = K + NI * kKey;
+    static constexpr size_t P = Q + NI * kKey;             // three planes [i][j]
+    static constexpr size_t size = P + 3 * kTri;
+    static_assert(N % 128 == 0 && size % 128 == 0, "tiles start on 128-byte boundaries");
+};
 
 struct BwdParams {
     const void *q, *k, *v, *dout;
@@ -55,9 +90,13 @@ struct BwdParams {
     void *dq, *dk_, *dv_;
     float *dbeta, *ddecay, *dstate_in;
     // workspace of this launch's heads, one entry per (direction, head, chunk)
-    float *X, *P, *N, *H0, *dH1, *W, *Z;
+    unsigned char *unit;       // Unit<DK, NI>
+    unsigned char *vt;         // [slice][64 tokens][64 columns] of the input type
+    unsigned char *ot;         // [slice][NI planes][64 tokens][64 columns]
+    float *HT, *GT;            // [dv][DK]: H0 and dH1, transposed
+    float *WT, *ZT;            // [dv][64 tokens]
     int head0, heads;          // the heads [head0, head0 + heads) of B*H
-    int BH, T, nc, dk, dv, dirs;
+    int BH, T, nc, dk, dv, dirs, slices;
 };
 
 // A chunk of one scan: its tokens in scan order.  Chunks are tiles [64 c, 64 c + n) of the sequence for
@@ -79,18 +118,207 @@ __device__ __forceinline__ Tile make_tile(const BwdParams &p, int dir, int local
     return t;
 }
 
-// Gates of a tile: b, a (clamped as in the forward kernels; 1 behind the sequence's end, where b = 0) and the
-// running sums of log2 a.  The sums are held in 64 bits: a strong decay brings them to several
-// hundred within a chunk, where 32 bits would leave differences of neighbours 1e-5 off.
-struct Gates {
-    double G[kC];
-    float a[kC], b[kC], gam[kC], e[kC];
+// ---------------------------------------------------------------- terms, fragments, products
+// two values as packed bf16 pairs (x in the low half): terms of x and y
+template <int NT>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&out)[NT])
+{
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+        out[t] = *reinterpret_cast<const uint32_t *>(&v);
+        if (t + 1 < NT) {
+            x -= __uint_as_float(out[t] << 16);
+            y -= __uint_as_float(out[t] & 0xffff0000u);
+        }
+    }
+}
+
+__device__ __forceinline__ float lo16(uint32_t u) { return __uint_as_float(u << 16); }
+__device__ __forceinline__ float hi16(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
+
+// byte offset of the 16-byte piece `piece` of row `row` in a swizzled tile with RB-byte rows
+template <int RB>
+__device__ __forceinline__ uint32_t sw(int row, int piece) { return row * RB + ((piece ^ (row & 7)) << 4); }
+
+__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr)
+{
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// c += A B.  The tensor core's fp32 sums are truncated, not rounded.
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Fragments of a 16 x 16 block of a tile at shared address `tile`.  A from [m][k] storage, A from [k][m] storage; B
+// (two n8 halves: r[0], r[1] and r[2], r[3]) from [n][k] storage, B from [k][n] storage.
+template <int RB>
+__device__ __forceinline__ void frag_a(uint32_t (&r)[4], uint32_t tile, int m, int k)
+{
+    const int l = threadIdx.x & 31;
+    ldsm(r, tile + sw<RB>(m + (l & 15), (k >> 3) + (l >> 4)));
+}
+template <int RB>
+__device__ __forceinline__ void frag_at(uint32_t (&r)[4], uint32_t tile, int m, int k)
+{
+    const int l = threadIdx.x & 31;
+    ldsm_t(r, tile + sw<RB>(k + (l & 7) + ((l >> 4) << 3), (m >> 3) + ((l >> 3) & 1)));
+}
+template <int RB>
+__device__ __forceinline__ void frag_b(uint32_t (&r)[4], uint32_t tile, int k, int n)
+{
+    const int l = threadIdx.x & 31;
+    ldsm(r, tile + sw<RB>(n + (l & 7) + ((l >> 4) << 3), (k >> 3) + ((l >> 3) & 1)));
+}
+template <int RB>
+__device__ __forceinline__ void frag_bt(uint32_t (&r)[4], uint32_t tile, int k, int n)
+{
+    const int l = threadIdx.x & 31;
+    ldsm_t(r, tile + sw<RB>(k + (l & 15), (n >> 3) + (l >> 4)));
+}
+
+// c (m16 x n16, two n8 tiles) += A B over the terms: products of order i + j < 3 (one term each: 0), the small ones
+// first and all into a sum of their own, which an ordinary addition, rounded to nearest, adds to c: the truncation of
+// the tensor core's sums then touches every 16 products once and does not pile up over k.
+template <int NA, int NB>
+__device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4])
+{
+    float d0[4] = {}, d1[4] = {};
+#pragma unroll
+    for (int order = NA + NB - 2 < 2 ? NA + NB - 2 : 2; order >= 0; --order)
+#pragma unroll
+        for (int i = 0; i < NA; ++i) {
+            const int j = order - i;
+            if (j < 0 || j >= NB) continue;
+            mma(d0, a[i], b[j][0], b[j][1]);
+            mma(d1, a[i], b[j][2], b[j][3]);
+        }
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+        c0[x] += d0[x];
+        c1[x] += d1[x];
+    }
+}
+
+// the left operand whose columns k .. k + 15 are the accumulator tiles x, y times per-column factors
+// f[0..1] (columns 2 t, 2 t + 1 of x) and f[2..3] (of y)
+template <int NT>
+__device__ __forceinline__ void acc_to_a(uint32_t (&a)[NT][4], const float (&x)[4], const float (&y)[4], const float (&f)[4])
+{
+    uint32_t u[NT];
+    split2<NT>(x[0] * f[0], x[1] * f[1], u);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) a[t][0] = u[t];
+    split2<NT>(x[2] * f[0], x[3] * f[1], u);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) a[t][1] = u[t];
+    split2<NT>(y[0] * f[2], y[1] * f[3], u);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) a[t][2] = u[t];
+    split2<NT>(y[2] * f[2], y[3] * f[3], u);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) a[t][3] = u[t];
+}
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void copy_block(uint32_t dst, const unsigned char *src, int bytes)
+{
+    for (int o = threadIdx.x * 16; o < bytes; o += blockDim.x * 16) copy16(dst + o, src + o);
+}
+
+__device__ __forceinline__ float warp_sum(float x)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+    return x;
+}
+
+// ---------------------------------------------------------------- prepare
+// Grid (chunks, heads, directions), 256 threads.
+template <int DK, int NI>
+struct PrepSmem {
+    unsigned char K[NI * Unit<DK, NI>::kKey];
+    unsigned char Q[NI * Unit<DK, NI>::kKey];
+    unsigned char Np[3 * kTri];
+    unsigned char Pp[3 * kTri];
+    float X[kC * (kC + 4)];        // X diag(b)
+    float N[kC * (kC + 4)];
+    Gates g;
 };
 
-__device__ __forceinline__ void load_gates(const BwdParams &p, const Tile &t, Gates &g)
+constexpr int kPrepThreads = 256;
+
+// eight values of a row as term planes in a swizzled tile (and its copy in the workspace)
+template <int NI, int RB, typename T>
+__device__ __forceinline__ void put8(const float (&x)[8], int row, int piece, unsigned char *smem, unsigned char *ws, size_t plane)
 {
-    if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
+    uint32_t w[NI][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t u[NI];
+        split2<NI>(x[2 * i], x[2 * i + 1], u);
+#pragma unroll
+        for (int t = 0; t < NI; ++t) w[t][i] = u[t];
+    }
+    const uint32_t o = sw<RB>(row, piece);
+#pragma unroll
+    for (int t = 0; t < NI; ++t) {
+        const uint4 v = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+        if (smem) *reinterpret_cast<uint4 *>(smem + t * plane + o) = v;
+        *reinterpret_cast<uint4 *>(ws + t * plane + o) = v;
+    }
+}
+
+// eight consecutive values of a row of `len`, zero behind its end (len is a multiple of 32)
+template <typename T>
+__device__ __forceinline__ void get8(const T *row, bool on, int c, int len, float (&x)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 0.f;
+    if (!on || c >= len) return;
+    if constexpr (sizeof(T) == 2) {
+        const uint4 u = *reinterpret_cast<const uint4 *>(row + c);
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = lo16(w[i]);
+            x[2 * i + 1] = hi16(w[i]);
+        }
+    } else {
+        const float4 u = reinterpret_cast<const float4 *>(row + c)[0], v = reinterpret_cast<const float4 *>(row + c)[1];
+        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+    }
+}
+
+template <int DK, int NI, typename T>
+__global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_constant__ BwdParams p)
+{
+    extern __shared__ __align__(128) unsigned char raw[];
+    using U = Unit<DK, NI>;
+    PrepSmem<DK, NI> &s = *reinterpret_cast<PrepSmem<DK, NI> *>(raw);
+    constexpr int ld = kC + 4;
+    const Tile t = make_tile(p, blockIdx.z, blockIdx.y, blockIdx.x);
+    unsigned char *unit = p.unit + t.ws * U::size;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (warp == 0) {
         double l[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -101,537 +329,854 @@ __device__ __forceinline__ void load_gates(const BwdParams &p, const Tile &t, Ga
                 a = fmaxf(p.decay[at], 7.52316385e-37f);   // 2^-120
                 b = p.beta[at];
             }
-            g.a[i] = a;
-            g.b[i] = b;
+            s.g.a[i] = a;
+            s.g.b[i] = b;
             l[h] = (double)log2f(a);
         }
-        double s = l[0] + l[1];
+        double sum = l[0] + l[1];
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, s, o);
-            if (lane >= o) s += y;
+            const double y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
         }
-        const double end = __shfl_sync(0xffffffffu, s, 31);
-        g.G[2 * lane] = s - l[1];
-        g.G[2 * lane + 1] = s;
-        g.gam[2 * lane] = exp2f((float)(s - l[1]));
-        g.gam[2 * lane + 1] = exp2f((float)s);
-        g.e[2 * lane] = exp2f((float)(end - (s - l[1])));
-        g.e[2 * lane + 1] = exp2f((float)(end - s));
+        const double end = __shfl_sync(0xffffffffu, sum, 31), first = sum - l[1];
+        s.g.G[2 * lane] = first;
+        s.g.G[2 * lane + 1] = sum;
+        s.g.gam[2 * lane] = exp2f((float)first);
+        s.g.gam[2 * lane + 1] = exp2f((float)sum);
+        s.g.e[2 * lane] = exp2f((float)(end - first));
+        s.g.e[2 * lane + 1] = exp2f((float)(end - sum));
     }
-}
-
-// rows i < 64 of x (row length `len` in memory, columns [c0, c0 + COLS)), zero where there is nothing
-template <int COLS, typename T>
-__device__ __forceinline__ void load_rows(const T *x, int len, int c0, const Tile &t, int T_, float *dst, int ld)
-{
-    const T *base = x + (size_t)t.head * T_ * len + c0;
-    for (int e = threadIdx.x; e < kC * COLS; e += kThreads) {
-        const int i = e / COLS, j = e % COLS;
-        dst[i * ld + j] = (i < t.n && c0 + j < len) ? ldf(base + (size_t)t.tok(i) * len + j) : 0.f;
+    const T *kb = static_cast<const T *>(p.k) + (size_t)t.head * p.T * p.dk;
+    const T *qb = static_cast<const T *>(p.q) + (size_t)t.head * p.T * p.dk;
+    for (int e = tid; e < kC * (DK / 8); e += kPrepThreads) {
+        const int i = e / (DK / 8), c = e % (DK / 8);
+        const bool on = i < t.n;
+        const size_t row = on ? (size_t)t.tok(i) * p.dk : 0;
+        float x[8];
+        get8(kb + row, on, 8 * c, p.dk, x);
+        put8<NI, DK * 2, T>(x, i, c, s.K, unit + U::K, U::kKey);
+        get8(qb + row, on, 8 * c, p.dk, x);
+        put8<NI, DK * 2, T>(x, i, c, s.Q, unit + U::Q, U::kKey);
     }
-}
-
-// acc[i][j] += sum_k A[m_i][k] B[k][n_j]  (TA: A[k][m_i]),  m_i = ty + TY i,  n_j = 4 tx + j;
-// the block's threads are TX x TY with TX = N / 4.
-template <int M, int N, bool TA, int RM>
-__device__ __forceinline__ void gemm(float (&acc)[RM][4], const float *A, int lda, const float *B, int ldb, int K)
-{
-    constexpr int TX = N / 4, TY = kThreads / TX;
-    static_assert(RM * TY == M, "tile");
-    const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
-    for (int k = 0; k < K; k += 4) {
-        float4 b[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) b[u] = *reinterpret_cast<const float4 *>(B + (k + u) * ldb + 4 * tx);
-#pragma unroll
-        for (int i = 0; i < RM; ++i) {
-            const int m = ty + TY * i;
-            float a[4];
-            if (TA) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) a[u] = A[(k + u) * lda + m];
-            } else {
-                const float4 x = *reinterpret_cast<const float4 *>(A + m * lda + k);
-                a[0] = x.x; a[1] = x.y; a[2] = x.z; a[3] = x.w;
-            }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                acc[i][0] = fmaf(a[u], b[u].x, acc[i][0]);
-                acc[i][1] = fmaf(a[u], b[u].y, acc[i][1]);
-                acc[i][2] = fmaf(a[u], b[u].z, acc[i][2]);
-                acc[i][3] = fmaf(a[u], b[u].w, acc[i][3]);
-            }
+    const T *vb = static_cast<const T *>(p.v) + (size_t)t.head * p.T * p.dv;
+    const T *ob = static_cast<const T *>(p.dout) + (size_t)t.head * p.T * p.dv;
+    for (int e = tid; e < p.slices * kC * 8; e += kPrepThreads) {
+        const int sl = e / (kC * 8), i = e / 8 % kC, c = e % 8;
+        const bool on = i < t.n;
+        const size_t row = on ? (size_t)t.tok(i) * p.dv : 0;
+        float x[8];
+        get8(ob + row, on, sl * kSlice + 8 * c, p.dv, x);
+        put8<NI, 128, T>(x, i, c, nullptr, p.ot + (t.ws * p.slices + sl) * (NI * kC * 128), kC * 128);
+        get8(vb + row, on, sl * kSlice + 8 * c, p.dv, x);
+        unsigned char *vt = p.vt + (t.ws * p.slices + sl) * (kC * kSlice * sizeof(T));
+        if constexpr (sizeof(T) == 2) {
+            put8<1, 128, T>(x, i, c, nullptr, vt, 0);
+        } else {
+            *reinterpret_cast<float4 *>(vt + sw<256>(i, 2 * c)) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4 *>(vt + sw<256>(i, 2 * c + 1)) = make_float4(x[4], x[5], x[6], x[7]);
         }
     }
-}
-
-template <int M, int N, int RM, typename F>
-__device__ __forceinline__ void each(const float (&acc)[RM][4], F f)
-{
-    constexpr int TX = N / 4, TY = kThreads / TX;
-    const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
-#pragma unroll
-    for (int i = 0; i < RM; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) f(ty + TY * i, 4 * tx + j, acc[i][j]);
-}
-
-template <int RM>
-__device__ __forceinline__ void zero(float (&acc)[RM][4])
-{
-#pragma unroll
-    for (int i = 0; i < RM; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
-}
-
-// ---------------------------------------------------------------- prepare
-// X, P, N of one chunk: grid (chunks, heads, directions).
-template <int DK>
-struct PrepSmem {
-    float K[kC * (DK + 4)];
-    float Q[kC * (DK + 4)];
-    float KT[DK * kLdC];
-    float X[kC * kLdC];        // X, then X diag(b)
-    float N[kC * kLdC];
-    Gates g;
-};
-
-template <int DK, typename T>
-__global__ void __launch_bounds__(kThreads) bwd_prepare_kernel(BwdParams p)
-{
-    extern __shared__ __align__(16) unsigned char raw[];
-    PrepSmem<DK> &s = *reinterpret_cast<PrepSmem<DK> *>(raw);
-    const Tile t = make_tile(p, blockIdx.z, blockIdx.y, blockIdx.x);
-    constexpr int ld = DK + 4;
-    load_gates(p, t, s.g);
-    load_rows<DK>(static_cast<const T *>(p.k), p.dk, 0, t, p.T, s.K, ld);
-    load_rows<DK>(static_cast<const T *>(p.q), p.dk, 0, t, p.T, s.Q, ld);
     __syncthreads();
-    for (int e = threadIdx.x; e < kC * DK; e += kThreads) s.KT[(e / kC) * kLdC + e % kC] = s.K[(e % kC) * ld + e / kC];
-    __syncthreads();
-    float kk[4][4], qk[4][4];
-    zero(kk);
-    zero(qk);
-    gemm<kC, kC, false>(kk, s.K, ld, s.KT, kLdC, DK);
-    gemm<kC, kC, false>(qk, s.Q, ld, s.KT, kLdC, DK);
-    float *Xg = p.X + t.ws * kC * kC, *Pg = p.P + t.ws * kC * kC, *Ng = p.N + t.ws * kC * kC;
-    each<kC, kC>(kk, [&](int i, int j, float x) {
-        const float y = j < i ? x * exp2f((float)(s.g.G[i] - s.g.G[j])) : 0.f;
-        Xg[i * kC + j] = y;
-        s.N[i * kLdC + j] = y;
-        s.X[i * kLdC + j] = y * s.g.b[j];
-    });
-    each<kC, kC>(qk, [&](int i, int j, float x) {
-        Pg[i * kC + j] = j <= i ? x * exp2f((float)(s.g.G[i] - s.g.G[j])) : 0.f;
-    });
+    if (tid < (int)sizeof(Gates) / 16)
+        reinterpret_cast<uint4 *>(unit + U::gates)[tid] = reinterpret_cast<const uint4 *>(&s.g)[tid];
+
+    // K K^T and Q K^T: warp w has rows 16 (w % 4) .. and columns 32 (w / 4) .., lower triangle only
+    const int wm = warp & 3, wn = warp >> 2;
+    const uint32_t ks = ptx::smem_u32(s.K), qs = ptx::smem_u32(s.Q);
+    float kk[4][4] = {}, qk[4][4] = {};
+#pragma unroll 2
+    for (int k = 0; k < DK; k += 16) {
+        uint32_t ka[NI][4], qa[NI][4];
+#pragma unroll
+        for (int x = 0; x < NI; ++x) {
+            frag_a<DK * 2>(ka[x], ks + x * U::kKey, 16 * wm, k);
+            frag_a<DK * 2>(qa[x], qs + x * U::kKey, 16 * wm, k);
+        }
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int nb = 32 * wn + 16 * n;
+            if (nb > 16 * wm) continue;
+            uint32_t b[NI][4];
+#pragma unroll
+            for (int x = 0; x < NI; ++x) frag_b<DK * 2>(b[x], ks + x * U::kKey, k, nb);
+            mma_terms(kk[2 * n], kk[2 * n + 1], ka, b);
+            mma_terms(qk[2 * n], qk[2 * n + 1], qa, b);
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < 4; ++n)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = 16 * wm + (lane >> 2) + 8 * h, j = 32 * wn + 8 * n + 2 * (lane & 3);
+            float x[2], y[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float d = j + c <= i ? exp2f((float)(s.g.G[i] - s.g.G[j + c])) : 0.f;
+                x[c] = j + c < i ? kk[n][2 * h + c] * d : 0.f;
+                y[c] = qk[n][2 * h + c] * d;
+                s.N[i * ld + j + c] = x[c];
+                s.X[i * ld + j + c] = x[c] * s.g.b[j + c];
+            }
+            uint32_t u[3];
+            split2<3>(y[0], y[1], u);
+#pragma unroll
+            for (int x3 = 0; x3 < 3; ++x3)
+                *reinterpret_cast<uint32_t *>(s.Pp + x3 * kTri + sw<128>(i, j >> 3) + (j & 7) * 2) = u[x3];
+        }
     __syncthreads();
     // N <- X - (X diag(b)) N in block rows of 16: the rows above by all threads, the 16 x 16 triangle by one
     // thread per column
     for (int r = 0; r < kC; r += 16) {
-        for (int e = threadIdx.x; e < 16 * kC; e += kThreads) {
-            const int i = r + e / kC, j = e % kC;
-            float y = s.N[i * kLdC + j];
-            for (int l = 0; l < r; ++l) y = fmaf(-s.X[i * kLdC + l], s.N[l * kLdC + j], y);
-            s.N[i * kLdC + j] = y;
+        if (r) {
+            const int i = r + (tid >> 4), j = 4 * (tid & 15);
+            float4 y = *reinterpret_cast<float4 *>(&s.N[i * ld + j]);
+            for (int l = 0; l < r; l += 4) {
+                const float4 x = *reinterpret_cast<const float4 *>(&s.X[i * ld + l]);
+                const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const float4 n = *reinterpret_cast<const float4 *>(&s.N[(l + u) * ld + j]);
+                    y.x = fmaf(-xs[u], n.x, y.x);
+                    y.y = fmaf(-xs[u], n.y, y.y);
+                    y.z = fmaf(-xs[u], n.z, y.z);
+                    y.w = fmaf(-xs[u], n.w, y.w);
+                }
+            }
+            *reinterpret_cast<float4 *>(&s.N[i * ld + j]) = y;
+            __syncthreads();
         }
-        __syncthreads();
-        if (threadIdx.x < kC) {
-            const int j = threadIdx.x;
+        if (tid < kC) {
+            const int j = tid;
             float y[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                y[i] = s.N[(r + i) * kLdC + j];
+                y[i] = s.N[(r + i) * ld + j];
 #pragma unroll
-                for (int l = 0; l < i; ++l) y[i] = fmaf(-s.X[(r + i) * kLdC + r + l], y[l], y[i]);
-                s.N[(r + i) * kLdC + j] = y[i];
+                for (int l = 0; l < i; ++l) y[i] = fmaf(-s.X[(r + i) * ld + r + l], y[l], y[i]);
+                s.N[(r + i) * ld + j] = y[i];
             }
         }
         __syncthreads();
     }
-    for (int e = threadIdx.x; e < kC * kC; e += kThreads) Ng[e] = s.N[(e / kC) * kLdC + e % kC];
+    for (int e = tid; e < kC * kC / 2; e += kPrepThreads) {
+        const int i = e / (kC / 2), j = 2 * (e % (kC / 2));
+        uint32_t u[3];
+        split2<3>(s.N[i * ld + j], s.N[i * ld + j + 1], u);
+#pragma unroll
+        for (int x = 0; x < 3; ++x)
+            *reinterpret_cast<uint32_t *>(s.Np + x * kTri + sw<128>(i, j >> 3) + (j & 7) * 2) = u[x];
+    }
+    __syncthreads();
+    for (int o = tid * 16; o < 3 * kTri; o += kPrepThreads * 16) {
+        *reinterpret_cast<uint4 *>(unit + U::N + o) = *reinterpret_cast<const uint4 *>(s.Np + o);
+        *reinterpret_cast<uint4 *>(unit + U::P + o) = *reinterpret_cast<const uint4 *>(s.Pp + o);
+    }
 }
 
 // ---------------------------------------------------------------- chains
-// Grid (slices, heads, 2 directions-and-walks): the forward walk stores H0 and W of every chunk, the backward
-// walk dH1 and Z.  The state slice (dk x 32) stays in registers and is mirrored in shared memory, where the
-// products read it.
-template <int DK>
-struct ChainSmem {
-    float K[kC * (DK + 4)];
-    float Q[kC * (DK + 4)];    // backward walk
-    float H[DK * kLdS];
-    float V[kC * kLdS];        // V or dO
-    float R[kC * kLdS];
-    float S[kC * kLdS];        // second 64 x 32 operand
-    float N[kC * kLdC];
-    float P[kC * kLdC];
-    Gates g;
+// Grid (slices of 64 columns, heads, direction and walk), four warps of 16 columns each.
+constexpr int kChainThreads = 128;
+
+// bytes of one stage: the unit's tiles from its start (forward: gates, N, K; backward: all) and the slice's V or dO
+template <int DK, int NI, typename T, int WALK>
+struct Stage {
+    using U = Unit<DK, NI>;
+    static constexpr int head = WALK ? (int)U::size : (int)U::Q;
+    static constexpr int tile = WALK ? NI * kC * 128 : kC * kSlice * (int)sizeof(T);
+    static constexpr int size = head + tile;
+    static constexpr int buffers = 2 * size <= 227 * 1024 ? 2 : 1;
 };
 
-template <int DK, typename T>
-__global__ void __launch_bounds__(kThreads) bwd_chain_kernel(BwdParams p)
+// r (16 x 64, columns tokens) += h^T-fragments times K^T
+template <int DK, int NI>
+__device__ __forceinline__ void state_times_keys(float (&r)[8][4], const float (&h)[DK / 8][4], uint32_t K)
 {
-    extern __shared__ __align__(16) unsigned char raw[];
-    ChainSmem<DK> &s = *reinterpret_cast<ChainSmem<DK> *>(raw);
-    constexpr int ld = DK + 4, RH = DK / 32;
-    const int dir = blockIdx.z >> 1, walk = blockIdx.z & 1, local = blockIdx.y, c0 = blockIdx.x * kSl;
-    const int head = p.head0 + local;
+    const float one[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+    for (int k = 0; k < DK / 16; ++k) {
+        uint32_t a[3][4];
+        acc_to_a<3>(a, h[2 * k], h[2 * k + 1], one);
+#pragma unroll
+        for (int n = 0; n < 4; ++n) {
+            uint32_t b[NI][4];
+#pragma unroll
+            for (int x = 0; x < NI; ++x) frag_b<DK * 2>(b[x], K + x * (int)Unit<DK, NI>::kKey, 16 * k, 16 * n);
+            mma_terms(r[2 * n], r[2 * n + 1], a, b);
+        }
+    }
+}
+
+// h (16 x dk) += A X, A the 16 x 16 left operand of tokens 16 k .. (terms), X the tile K or Q
+template <int DK, int NI, int NA>
+__device__ __forceinline__ void add_outer(float (&h)[DK / 8][4], const uint32_t (&a)[NA][4], uint32_t X, int k)
+{
+#pragma unroll
+    for (int n = 0; n < DK / 16; ++n) {
+        uint32_t b[NI][4];
+#pragma unroll
+        for (int x = 0; x < NI; ++x) frag_bt<DK * 2>(b[x], X + x * (int)Unit<DK, NI>::kKey, 16 * k, 16 * n);
+        mma_terms(h[2 * n], h[2 * n + 1], a, b);
+    }
+}
+
+template <int DK, int NI, typename T, int WALK>
+__device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char *raw)
+{
+    using U = Unit<DK, NI>;
+    using S = Stage<DK, NI, T, WALK>;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q2 = 2 * (lane & 3);
+    const int local = blockIdx.y, head = p.head0 + local, sl = blockIdx.x;
+    const int row = sl * kSlice + 16 * warp;                   // this warp's columns of dv: rows of H^T
+    const bool on = row < p.dv;
     const size_t st = (size_t)p.dk * p.dv;
-    float h[RH][4];
-    zero(h);
+    float h[DK / 8][4];
     const float *init = nullptr;
-    if (walk == 0 && dir == 0 && p.state_in) init = p.state_in + head * st;
-    if (walk == 1 && p.dstate) init = p.dstate + ((size_t)dir * p.BH + head) * st;
-    {
-        const int tx = threadIdx.x % 8, ty = threadIdx.x / 8;
+    if (WALK == 0 && dir == 0 && p.state_in) init = p.state_in + head * st;
+    if (WALK == 1 && p.dstate) init = p.dstate + ((size_t)dir * p.BH + head) * st;
 #pragma unroll
-        for (int i = 0; i < RH; ++i)
+    for (int n = 0; n < DK / 8; ++n)
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (init && ty + 32 * i < p.dk) h[i][j] = init[(size_t)(ty + 32 * i) * p.dv + c0 + 4 * tx + j];
-    }
+        for (int x = 0; x < 4; ++x) {
+            const int kx = 8 * n + q2 + (x & 1), vx = row + g + 8 * (x >> 1);
+            h[n][x] = init && on && kx < p.dk ? init[(size_t)kx * p.dv + vx] : 0.f;
+        }
+
+    const uint32_t base = ptx::smem_u32(raw);
+    auto fetch = [&](int step) {
+        const int c = (dir ^ WALK) ? p.nc - 1 - step : step;
+        const size_t ws = ((size_t)dir * p.heads + local) * p.nc + c;
+        const uint32_t dst = base + (step % S::buffers) * S::size;
+        copy_block(dst, p.unit + ws * U::size, S::head);
+        copy_block(dst + S::head, (WALK ? p.ot : p.vt) + (ws * p.slices + sl) * S::tile, S::tile);
+        copy_commit();
+    };
+    if (S::buffers == 2) fetch(0);
     for (int step = 0; step < p.nc; ++step) {
-        const int c = (dir ^ walk) ? p.nc - 1 - step : step;
-        const Tile t = make_tile(p, dir, local, c);
-        float *keep = (walk ? p.dH1 : p.H0) + t.ws * st + c0;
-        each<DK, kSl>(h, [&](int i, int j, float x) {
-            s.H[i * kLdS + j] = x;
-            if (i < p.dk) keep[(size_t)i * p.dv + j] = x;
-        });
-        load_gates(p, t, s.g);
-        load_rows<DK>(static_cast<const T *>(p.k), p.dk, 0, t, p.T, s.K, ld);
-        load_rows<kSl>(static_cast<const T *>(walk ? p.dout : p.v), p.dv, c0, t, p.T, s.V, kLdS);
-        if (walk) load_rows<DK>(static_cast<const T *>(p.q), p.dk, 0, t, p.T, s.Q, ld);
-        const float *Ng = p.N + t.ws * kC * kC, *Pg = p.P + t.ws * kC * kC;
-        for (int e = threadIdx.x; e < kC * kC; e += kThreads) {
-            s.N[(e / kC) * kLdC + e % kC] = Ng[e];
-            if (walk) s.P[(e / kC) * kLdC + e % kC] = Pg[e];
+        const int c = (dir ^ WALK) ? p.nc - 1 - step : step;
+        const size_t ws = ((size_t)dir * p.heads + local) * p.nc + c;
+        if (S::buffers == 1) {
+            __syncthreads();
+            fetch(step);
         }
+        copy_wait<0>();
         __syncthreads();
-        float r[2][4], m[2][4];
-        zero(r);
-        gemm<kC, kSl, false>(r, s.K, ld, s.H, kLdS, DK);
-        float *out = (walk ? p.Z : p.W) + t.ws * kC * p.dv + c0;
-        const float gend = s.g.gam[kC - 1];
-        if (walk == 0) {
-            each<kC, kSl>(r, [&](int i, int j, float x) { s.R[i * kLdS + j] = s.V[i * kLdS + j] - s.g.gam[i] * x; });
-            __syncthreads();
-            each<kC, kSl>(r, [&](int i, int j, float) { s.S[i * kLdS + j] = s.g.b[i] * s.R[i * kLdS + j]; });
-            __syncthreads();
-            zero(m);
-            gemm<kC, kSl, false>(m, s.N, kLdC, s.S, kLdS, kC);
-            __syncthreads();
-            each<kC, kSl>(m, [&](int i, int j, float x) {
-                const float w = s.R[i * kLdS + j] - x;
-                out[(size_t)i * p.dv + j] = w;
-                s.S[i * kLdS + j] = s.g.e[i] * s.g.b[i] * w;
-            });
-            __syncthreads();
+        if (S::buffers == 2 && step + 1 < p.nc) fetch(step + 1);   // into the stage that all warps have left
+        if (!on) continue;
+        const int so = (step % S::buffers) * S::size;
+        const Gates &gt = *reinterpret_cast<const Gates *>(raw + so);
+        const uint32_t tN = base + so + (uint32_t)U::N, tK = base + so + (uint32_t)U::K, tX = base + so + S::head;
+        {
+            float *keep = (WALK ? p.GT : p.HT) + (ws * p.dv + row) * DK;
 #pragma unroll
-            for (int i = 0; i < RH; ++i)
+            for (int n = 0; n < DK / 8; ++n) {
+                st2(keep + (size_t)g * DK + 8 * n + q2, h[n][0], h[n][1]);
+                st2(keep + (size_t)(g + 8) * DK + 8 * n + q2, h[n][2], h[n][3]);
+            }
+        }
+        float r[8][4] = {}, w[8][4];
+        state_times_keys<DK, NI>(r, h, tK);
+        const float gend = gt.gam[kC - 1];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h[i][j] *= gend;
-            gemm<DK, kSl, true>(h, s.K, ld, s.S, kLdS, kC);
+        for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) h[n][x] *= gend;
+        float *out = (WALK ? p.ZT : p.WT) + (ws * p.dv + row) * kC;
+        if (WALK == 0) {
+            // R = V - gam (H^T K^T)
+            const unsigned char *vt = raw + so + S::head;
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int i = 8 * n + q2 + (x & 1), v = 16 * warp + g + 8 * (x >> 1);
+                    constexpr int RB = kSlice * sizeof(T), per = 16 / sizeof(T);
+                    const float y = ldf(reinterpret_cast<const T *>(vt + sw<RB>(i, v / per)) + v % per);
+                    r[n][x] = y - gt.gam[i] * r[n][x];
+                    w[n][x] = r[n][x];
+                }
+            // W = R - N diag(b) R: tokens j = 16 k .. feed tokens i >= j
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float f[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) f[x] = -gt.b[16 * k + q2 + (x & 1) + 8 * (x >> 1)];
+                uint32_t a[3][4];
+                acc_to_a<3>(a, r[2 * k], r[2 * k + 1], f);
+#pragma unroll
+                for (int n = k; n < 4; ++n) {
+                    uint32_t b[3][4];
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) frag_b<128>(b[x], tN + x * kTri, 16 * k, 16 * n);
+                    mma_terms(w[2 * n], w[2 * n + 1], a, b);
+                }
+            }
+            // H <- gam_C H + K^T diag(e b) W
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float f[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int i = 16 * k + q2 + (x & 1) + 8 * (x >> 1);
+                    f[x] = gt.e[i] * gt.b[i];
+                }
+                uint32_t a[3][4];
+                acc_to_a<3>(a, w[2 * k], w[2 * k + 1], f);
+                add_outer<DK, NI>(h, a, tK, k);
+            }
         } else {
-            zero(m);
-            gemm<kC, kSl, true>(m, s.P, kLdC, s.V, kLdS, kC);
-            each<kC, kSl>(r, [&](int i, int j, float x) { s.R[i * kLdS + j] = s.g.e[i] * x; });
-            __syncthreads();
-            each<kC, kSl>(m, [&](int i, int j, float x) {
-                const float du = s.R[i * kLdS + j] + x;
-                s.R[i * kLdS + j] = du;
-                s.S[i * kLdS + j] = s.g.b[i] * du;
-            });
-            __syncthreads();
-            zero(m);
-            gemm<kC, kSl, true>(m, s.N, kLdC, s.S, kLdS, kC);
-            __syncthreads();
-            each<kC, kSl>(m, [&](int i, int j, float x) {
-                const float z = s.R[i * kLdS + j] - x;
-                out[(size_t)i * p.dv + j] = z;
-                s.S[i * kLdS + j] = -s.g.gam[i] * s.g.b[i] * z;
-                s.V[i * kLdS + j] *= s.g.gam[i];
-            });
-            __syncthreads();
+            const uint32_t tQ = base + so + (uint32_t)U::Q, tP = base + so + (uint32_t)U::P;
+            // dU = diag(e) K dH1 + P^T dO: tokens i = 16 k .. feed tokens j <= i; and dH += Q^T diag(gam) dO
 #pragma unroll
-            for (int i = 0; i < RH; ++i)
+            for (int n = 0; n < 8; ++n)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) h[i][j] *= gend;
-            gemm<DK, kSl, true>(h, s.K, ld, s.S, kLdS, kC);
-            gemm<DK, kSl, true>(h, s.Q, ld, s.V, kLdS, kC);
+                for (int x = 0; x < 4; ++x) r[n][x] *= gt.e[8 * n + q2 + (x & 1)];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                uint32_t o[NI][4], a[3][4];
+#pragma unroll
+                for (int x = 0; x < NI; ++x) frag_at<128>(o[x], tX + x * (kC * 128), 16 * warp, 16 * k);
+#pragma unroll
+                for (int n = 0; n <= k; ++n) {
+                    uint32_t b[3][4];
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) frag_bt<128>(b[x], tP + x * kTri, 16 * k, 16 * n);
+                    mma_terms(r[2 * n], r[2 * n + 1], o, b);
+                }
+                float f[4], u[4], v[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) f[x] = gt.gam[16 * k + q2 + (x & 1) + 8 * (x >> 1)];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) u[x] = v[x] = 0.f;
+#pragma unroll
+                for (int x = NI - 1; x >= 0; --x) {
+                    u[0] += lo16(o[x][0]); u[1] += hi16(o[x][0]); u[2] += lo16(o[x][1]); u[3] += hi16(o[x][1]);
+                    v[0] += lo16(o[x][2]); v[1] += hi16(o[x][2]); v[2] += lo16(o[x][3]); v[3] += hi16(o[x][3]);
+                }
+                acc_to_a<3>(a, u, v, f);
+                add_outer<DK, NI>(h, a, tQ, k);
+            }
+            // Z = dU - N^T diag(b) dU: tokens i = 16 k .. feed tokens j <= i
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) w[n][x] = r[n][x];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float f[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) f[x] = -gt.b[16 * k + q2 + (x & 1) + 8 * (x >> 1)];
+                uint32_t a[3][4];
+                acc_to_a<3>(a, r[2 * k], r[2 * k + 1], f);
+#pragma unroll
+                for (int n = 0; n <= k; ++n) {
+                    uint32_t b[3][4];
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) frag_bt<128>(b[x], tN + x * kTri, 16 * k, 16 * n);
+                    mma_terms(w[2 * n], w[2 * n + 1], a, b);
+                }
+            }
+            // dH -= K^T diag(gam b) Z
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float f[4];
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int i = 16 * k + q2 + (x & 1) + 8 * (x >> 1);
+                    f[x] = -gt.gam[i] * gt.b[i];
+                }
+                uint32_t a[3][4];
+                acc_to_a<3>(a, w[2 * k], w[2 * k + 1], f);
+                add_outer<DK, NI>(h, a, tK, k);
+            }
         }
-        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            st2(out + (size_t)g * kC + 8 * n + q2, w[n][0], w[n][1]);
+            st2(out + (size_t)(g + 8) * kC + 8 * n + q2, w[n][2], w[n][3]);
+        }
     }
-    if (walk == 1 && dir == 0 && p.dstate_in) {
-        float *out = p.dstate_in + head * st + c0;
-        each<DK, kSl>(h, [&](int i, int j, float x) {
-            if (i < p.dk) out[(size_t)i * p.dv + j] = x;
-        });
+    if (WALK == 1 && dir == 0 && on && p.dstate_in) {
+        float *to = p.dstate_in + head * st;
+#pragma unroll
+        for (int n = 0; n < DK / 8; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int kx = 8 * n + q2 + (x & 1), vx = row + g + 8 * (x >> 1);
+                if (kx < p.dk) to[(size_t)kx * p.dv + vx] = h[n][x];
+            }
     }
+}
+
+template <int DK, int NI, typename T>
+__global__ void __launch_bounds__(kChainThreads) bwd_chain_kernel(const __grid_constant__ BwdParams p)
+{
+    extern __shared__ __align__(128) unsigned char raw[];
+    // the backward walks, the longer ones, come first
+    if (blockIdx.z < p.dirs) chain<DK, NI, T, 1>(p, blockIdx.z, raw);
+    else chain<DK, NI, T, 0>(p, blockIdx.z - p.dirs, raw);
 }
 
 // ---------------------------------------------------------------- gradients
-// Grid (chunks, heads).  Walks the slices of dv, summing dO H0^T, Y H0^T, U dH1^T (64 x dk) and dO U^T, Y U^T
-// (64 x 64) in registers, then finishes dQ, dK and the gates.
-template <int DK>
+// Grid (chunks, heads), eight warps: warp w has the tokens 16 (w % 4) .. of every result and its columns' half w / 4.
+constexpr int kGradThreads = 256;
+constexpr int kStep = 32;              // dv columns per step of the walk over dv
+constexpr int kLdT = kC + 4;           // pitch of 64-wide fp32 rows
+
+template <int DK, int NI>
 struct GradSmem {
-    float K[kC * (DK + 4)];
-    float Q[kC * (DK + 4)];
-    float dq[kC * (DK + 4)];   // sums over the directions, rows by token
-    float dk[kC * (DK + 4)];
-    // during the walk: HT, GT (32 x dk: slices of H0 and dH1, transposed); behind it M (64 x 65)
-    static constexpr int kHT = kSl * (DK + 4);
-    float states[2 * kHT];
-    // during the walk: dO, Y = diag(b) Z, U = diag(b) W (64 x 32 each) and U^T; behind it E, F (64 x 64)
-    static constexpr int kRow = kC * kLdS;
-    float rows[3 * kRow + kSl * kLdC];
-    float m0[kC], m1[kC], db[2][kC], da[2][kC], red[kThreads / 32];
+    using U = Unit<DK, NI>;
+    static constexpr bool kStage = NI == 1;                    // room for the next step's fp32 tiles
+    static constexpr int NE = NI == 1 ? 2 : 3;                 // terms of E and F (results of NI = 1 are bf16)
+    static constexpr int kOTiles = NI == 1 ? 2 : 1;            // dO: every slice, or the walk's
+    static constexpr int kState = kStep * DK * 2, kVal = kStep * kC * 2;
+    struct Walk {                                              // term planes of the step's H0, dH1, U, Y: rows dv
+        unsigned char H[3 * kState], G[3 * kState], U[3 * kVal], Y[3 * kVal];
+    };
+    struct Tail {
+        unsigned char E[NE * kTri], S[NE * kTri];              // [i][j]
+        float F[kC * kLdT], M[kC * (kC + 1)];
+    };
     Gates g;
+    unsigned char K[NI * U::kKey], Q[NI * U::kKey];
+    unsigned char O[kOTiles * NI * kC * 128];
+    union {
+        Walk walk;
+        Tail tail;
+    };
+    float Z[kStep * kLdT], Z0[kStep * kLdT];                   // the step's Z; the first direction's
+    float W[kStage ? kStep * kLdT : 4];
+    float H[kStage ? kStep * DK : 4], GT[kStage ? kStep * DK : 4];
+    float db[kC], da[kC];                                      // over the directions, by token
+    float m0[2][kC], m1[2][kC], dbw[8][kC], col[8][kC], hh[8];
 };
 
-__device__ __forceinline__ float warp_sum(float x)
+// 32 rows of `len` floats to rows of pitch `ld`
+__device__ __forceinline__ void copy_rows(float *dst, int ld, const float *src, int len)
 {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
+    const int per = len / 4;
+    for (int e = threadIdx.x; e < kStep * per; e += kGradThreads)
+        copy16(ptx::smem_u32(dst + (e / per) * ld + 4 * (e % per)), src + (size_t)(e / per) * len + 4 * (e % per));
 }
 
-template <int DK, typename T>
-__global__ void __launch_bounds__(kThreads, 1) bwd_grad_kernel(BwdParams p)
+// 8 floats to term planes in a swizzled tile
+template <int RB>
+__device__ __forceinline__ void planes8(const float (&x)[8], int row, int piece, unsigned char *to, int plane)
 {
-    extern __shared__ __align__(16) unsigned char raw[];
-    GradSmem<DK> &s = *reinterpret_cast<GradSmem<DK> *>(raw);
-    static_assert(2 * kC * kLdC <= 3 * kC * kLdS + kSl * kLdC, "E and F fit in the slices' tiles");
-    static_assert(kC * (kC + 1) <= 2 * kSl * (DK + 4), "M fits in the state tiles");
-    float *const sHT = s.states, *const sGT = s.states + s.kHT, *const sM = s.states;
-    float *const sO = s.rows, *const sY = s.rows + s.kRow, *const sU = s.rows + 2 * s.kRow;
-    float *const sUT = s.rows + 3 * s.kRow, *const sE = s.rows, *const sF = s.rows + kC * kLdC;
-    constexpr int ld = DK + 4, RG = kC * DK / 4 / kThreads;
-    const size_t st = (size_t)p.dk * p.dv;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    for (int e = threadIdx.x; e < kC * ld; e += kThreads) s.dq[e] = s.dk[e] = 0.f;
-    if (threadIdx.x < kC) s.db[1][threadIdx.x] = s.da[1][threadIdx.x] = 0.f;
+    uint32_t w[3][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t u[3];
+        split2<3>(x[2 * i], x[2 * i + 1], u);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) w[t][i] = u[t];
+    }
+#pragma unroll
+    for (int t = 0; t < 3; ++t)
+        *reinterpret_cast<uint4 *>(to + t * plane + sw<RB>(row, piece)) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
+}
+
+__device__ __forceinline__ void get8f(const float *p, float (&x)[8])
+{
+    const float4 u = reinterpret_cast<const float4 *>(p)[0], v = reinterpret_cast<const float4 *>(p)[1];
+    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+    x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+}
+
+// columns j, j + 1 of row i of a tile of term planes
+template <int NI, int RB>
+__device__ __forceinline__ float2 pair_at(const unsigned char *tile, int plane, int i, int j)
+{
+    float2 r = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int x = NI - 1; x >= 0; --x) {
+        const uint32_t u = *reinterpret_cast<const uint32_t *>(tile + x * plane + sw<RB>(i, j >> 3) + (j & 7) * 2);
+        r.x += lo16(u);
+        r.y += hi16(u);
+    }
+    return r;
+}
+
+template <int DK, int NI, typename T>
+__global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_constant__ BwdParams p)
+{
+    extern __shared__ __align__(128) unsigned char raw[];
+    using U = Unit<DK, NI>;
+    using Sm = GradSmem<DK, NI>;
+    Sm &s = *reinterpret_cast<Sm *>(raw);
+    constexpr int NT = DK / 16, NE = Sm::NE;                   // n8 tiles of a warp's half of dk
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, wm = warp & 3, wn = warp >> 2;
+    const int g = lane >> 2, q2 = 2 * (lane & 3);
+    const uint32_t aK = ptx::smem_u32(s.K), aQ = ptx::smem_u32(s.Q), aO = ptx::smem_u32(s.O);
+    const uint32_t aH = ptx::smem_u32(s.walk.H), aG = ptx::smem_u32(s.walk.G), aU = ptx::smem_u32(s.walk.U), aY = ptx::smem_u32(s.walk.Y);
+    const uint32_t aE = ptx::smem_u32(s.tail.E), aS = ptx::smem_u32(s.tail.S);
+    const size_t first = ((size_t)blockIdx.y) * p.nc + blockIdx.x;   // this chunk in the first direction
+    float *const part = reinterpret_cast<float *>(p.unit + first * U::size);   // bidirectional: its dQ, dK sums
+    static_assert(2 * kC * DK * sizeof(float) <= U::size, "the first direction's sums fit in its unit");
+    if (tid < kC) s.db[tid] = s.da[tid] = 0.f;
 
     for (int dir = 0; dir < p.dirs; ++dir) {
         const Tile t = make_tile(p, dir, blockIdx.y, blockIdx.x);
-        const float *H0 = p.H0 + t.ws * st, *dH1 = p.dH1 + t.ws * st;
-        const float *Wg = p.W + t.ws * kC * p.dv, *Zg = p.Z + t.ws * kC * p.dv;
+        const unsigned char *unit = p.unit + t.ws * U::size;
+        const float *HT = p.HT + t.ws * p.dv * DK, *GT = p.GT + t.ws * p.dv * DK;
+        const float *WT = p.WT + t.ws * p.dv * kC, *ZT = p.ZT + t.ws * p.dv * kC, *ZT0 = p.ZT + first * p.dv * kC;
+        const bool last = dir == p.dirs - 1;
         __syncthreads();
-        load_gates(p, t, s.g);
-        load_rows<DK>(static_cast<const T *>(p.k), p.dk, 0, t, p.T, s.K, ld);
-        load_rows<DK>(static_cast<const T *>(p.q), p.dk, 0, t, p.T, s.Q, ld);
-        float hdo[RG][4], hy[RG][4], du1[RG][4], dp[4][4], dx[4][4];
-        zero(hdo);
-        zero(hy);
-        zero(du1);
-        zero(dp);
-        zero(dx);
-        float hh = 0.f, db[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) db[i] = 0.f;
-        for (int c0 = 0; c0 < p.dv; c0 += kSl) {
-            __syncthreads();
-            load_rows<kSl>(static_cast<const T *>(p.dout), p.dv, c0, t, p.T, sO, kLdS);
-            // one warp per row, one lane per column: the row's part of db = Z . W is a warp sum
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                const int i = warp + 8 * r;
-                const float w = Wg[(size_t)i * p.dv + c0 + lane], z = Zg[(size_t)i * p.dv + c0 + lane];
-                const float b = s.g.b[i];
-                sU[i * kLdS + lane] = b * w;
-                sUT[lane * kLdC + i] = b * w;
-                sY[i * kLdS + lane] = b * z;
-                db[r] = fmaf(z, w, db[r]);
+        auto fetch = [&](int c0) {
+            if constexpr (Sm::kStage) {
+                copy_rows(s.H, DK, HT + (size_t)c0 * DK, DK);
+                copy_rows(s.GT, DK, GT + (size_t)c0 * DK, DK);
+                copy_rows(s.W, kLdT, WT + (size_t)c0 * kC, kC);
             }
-            for (int e = threadIdx.x; e < DK * kSl; e += kThreads) {
-                const int i = e / kSl, j = e % kSl;
-                float x = 0.f, y = 0.f;
-                if (i < p.dk) {
-                    x = H0[(size_t)i * p.dv + c0 + j];
-                    y = dH1[(size_t)i * p.dv + c0 + j];
+            copy_rows(s.Z, kLdT, ZT + (size_t)c0 * kC, kC);
+            if (dir == 1) copy_rows(s.Z0, kLdT, ZT0 + (size_t)c0 * kC, kC);
+            if (!Sm::kStage && c0 % kSlice == 0)
+                copy_block(aO, p.ot + (t.ws * p.slices + c0 / kSlice) * (NI * kC * 128), NI * kC * 128);
+            copy_commit();
+        };
+        copy_block(ptx::smem_u32(&s.g), unit, sizeof(Gates));
+        copy_block(aK, unit + U::K, NI * (int)U::kKey);
+        copy_block(aQ, unit + U::Q, NI * (int)U::kKey);
+        if (Sm::kStage) copy_block(aO, p.ot + t.ws * p.slices * (NI * kC * 128), p.slices * NI * kC * 128);
+        fetch(0);
+
+        float hdo[NT][4] = {}, hy[NT][4] = {}, du[NT][4] = {}, dp[4][4] = {}, dx[4][4] = {}, db[8] = {}, hh = 0.f;
+        for (int c0 = 0; c0 < p.dv; c0 += kStep) {
+            copy_wait<0>();
+            __syncthreads();           // the step's tiles are here, and every warp has left the last step's planes
+            for (int e = tid; e < kStep * (DK / 8); e += kGradThreads) {
+                const int r = e / (DK / 8), c = e % (DK / 8);
+                float x[8], y[8];
+                get8f(Sm::kStage ? s.H + r * DK + 8 * c : HT + (size_t)(c0 + r) * DK + 8 * c, x);
+                get8f(Sm::kStage ? s.GT + r * DK + 8 * c : GT + (size_t)(c0 + r) * DK + 8 * c, y);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) hh = fmaf(x[i], y[i], hh);
+                planes8<DK * 2>(x, r, c, s.walk.H, Sm::kState);
+                planes8<DK * 2>(y, r, c, s.walk.G, Sm::kState);
+            }
+            {
+                const int r = tid >> 3, c = tid & 7;           // a column of dv, eight tokens
+                float w[8], z[8];
+                get8f(Sm::kStage ? s.W + r * kLdT + 8 * c : WT + (size_t)(c0 + r) * kC + 8 * c, w);
+                get8f(s.Z + r * kLdT + 8 * c, z);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    db[i] = fmaf(w[i], z[i], db[i]);
+                    w[i] *= s.g.b[8 * c + i];
+                    z[i] *= s.g.b[8 * c + i];
                 }
-                sHT[j * ld + i] = x;
-                sGT[j * ld + i] = y;
-                hh = fmaf(x, y, hh);
+                planes8<128>(w, r, c, s.walk.U, Sm::kVal);
+                planes8<128>(z, r, c, s.walk.Y, Sm::kVal);
+            }
+            if (last) {                // dV = Y, of both directions
+                for (int e = tid; e < t.n * (kStep / 2); e += kGradThreads) {
+                    const int i = e / (kStep / 2), j = 2 * (e % (kStep / 2));
+                    float x = s.Z[j * kLdT + i], y = s.Z[(j + 1) * kLdT + i];
+                    if (dir == 1) {
+                        x += s.Z0[j * kLdT + t.n - 1 - i];
+                        y += s.Z0[(j + 1) * kLdT + t.n - 1 - i];
+                    }
+                    st2(static_cast<T *>(p.dv_) + ((size_t)t.head * p.T + t.tok(i)) * p.dv + c0 + j, s.g.b[i] * x, s.g.b[i] * y);
+                }
             }
             __syncthreads();
-            gemm<kC, DK, false>(hdo, sO, kLdS, sHT, ld, kSl);
-            gemm<kC, DK, false>(hy, sY, kLdS, sHT, ld, kSl);
-            gemm<kC, DK, false>(du1, sU, kLdS, sGT, ld, kSl);
-            gemm<kC, kC, false>(dp, sO, kLdS, sUT, kLdC, kSl);
-            gemm<kC, kC, false>(dx, sY, kLdS, sUT, kLdC, kSl);
-            // dv = Y: a bidirectional call adds the second direction to what the first one keeps in Z
-            for (int e = threadIdx.x; e < kC * kSl; e += kThreads) {
-                const int i = e / kSl, j = e % kSl;
-                if (i >= t.n) continue;
-                const size_t at = ((size_t)t.head * p.T + t.tok(i)) * p.dv + c0 + j;
-                float y = sY[i * kLdS + j];
-                if (dir == 1) {
-                    const Tile f = make_tile(p, 0, blockIdx.y, blockIdx.x);
-                    const float b = p.beta[(size_t)t.head * p.T + t.tok(i)];
-                    y += b * p.Z[f.ws * kC * p.dv + (size_t)(t.n - 1 - i) * p.dv + c0 + j];
+            if (Sm::kStage && c0 + kStep < p.dv) fetch(c0 + kStep);
+#pragma unroll
+            for (int k = 0; k < kStep; k += 16) {
+                uint32_t o[NI][4], u[3][4], y[3][4];
+                const uint32_t ot = aO + (Sm::kStage ? c0 / kSlice : 0) * (NI * kC * 128);
+#pragma unroll
+                for (int x = 0; x < NI; ++x) frag_a<128>(o[x], ot + x * (kC * 128), 16 * wm, c0 % kSlice + k);
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    frag_at<128>(u[x], aU + x * Sm::kVal, 16 * wm, k);
+                    frag_at<128>(y[x], aY + x * Sm::kVal, 16 * wm, k);
                 }
-                if (dir == p.dirs - 1) stf(static_cast<T *>(p.dv_) + at, y);
+#pragma unroll
+                for (int n = 0; n < NT / 2; ++n) {
+                    uint32_t b[3][4];
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) frag_bt<DK * 2>(b[x], aH + x * Sm::kState, k, wn * (DK / 2) + 16 * n);
+                    mma_terms(hdo[2 * n], hdo[2 * n + 1], o, b);
+                    mma_terms(hy[2 * n], hy[2 * n + 1], y, b);
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) frag_bt<DK * 2>(b[x], aG + x * Sm::kState, k, wn * (DK / 2) + 16 * n);
+                    mma_terms(du[2 * n], du[2 * n + 1], u, b);
+                }
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    if (32 * wn + 16 * n > 16 * wm) continue;
+                    uint32_t b[3][4];
+#pragma unroll
+                    for (int x = 0; x < 3; ++x) frag_bt<128>(b[x], aU + x * Sm::kVal, k, 32 * wn + 16 * n);
+                    mma_terms(dp[2 * n], dp[2 * n + 1], o, b);
+                    mma_terms(dx[2 * n], dx[2 * n + 1], y, b);
+                }
+            }
+            if (!Sm::kStage && c0 + kStep < p.dv) {
+                __syncthreads();
+                fetch(c0 + kStep);
             }
         }
-        const float *Xg = p.X + t.ws * kC * kC, *Pg = p.P + t.ws * kC * kC;
-        __syncthreads();
+
+        // db_i = Z_i . W_i: over a warp's four columns of dv here, over the warps below; <H0, dH1> likewise
 #pragma unroll
-        for (int r = 0; r < 8; ++r) {
-            const float x = warp_sum(db[r]);
-            if (lane == 0) s.db[0][warp + 8 * r] = x;
+        for (int i = 0; i < 8; ++i) {
+            db[i] += __shfl_xor_sync(0xffffffffu, db[i], 8);
+            db[i] += __shfl_xor_sync(0xffffffffu, db[i], 16);
+            if (lane < 8) s.dbw[warp][8 * lane + i] = db[i];
         }
         hh = warp_sum(hh);
-        if (lane == 0) s.red[warp] = hh;
-        each<kC, kC>(dp, [&](int i, int j, float x) {
-            const bool on = j <= i;
-            sE[i * kLdC + j] = on ? x * exp2f((float)(s.g.G[i] - s.g.G[j])) : 0.f;
-            sM[i * (kC + 1) + j] = j < i ? x * Pg[i * kC + j] : 0.f;
-        });
-        each<kC, kC>(dx, [&](int i, int j, float x) {
-            sF[i * kLdC + j] = j < i ? -x * exp2f((float)(s.g.G[i] - s.g.G[j])) : 0.f;
-            if (j < i) sM[i * (kC + 1) + j] -= x * Xg[i * kC + j];
-        });
-        // m0_i = gam_i (q_i . hdo_i - k_i . hy_i), m1_i = e_i k_i . du1_i: sums over the row's threads
-        {
-            constexpr int TX = DK / 4, TY = kThreads / TX;
-            const int tx = threadIdx.x % TX, ty = threadIdx.x / TX;
+        if (lane == 0) s.hh[warp] = hh;
+        // X and P again, in the layout of dX and dP
+        float kk[4][4] = {}, qk[4][4] = {};
+#pragma unroll 2
+        for (int k = 0; k < DK; k += 16) {
+            uint32_t ka[NI][4], qa[NI][4];
 #pragma unroll
-            for (int i = 0; i < RG; ++i) {
-                const int m = ty + TY * i;
-                float x = 0.f, y = 0.f;
+            for (int x = 0; x < NI; ++x) {
+                frag_a<DK * 2>(ka[x], aK + x * (int)U::kKey, 16 * wm, k);
+                frag_a<DK * 2>(qa[x], aQ + x * (int)U::kKey, 16 * wm, k);
+            }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float k = s.K[m * ld + 4 * tx + j];
-                    x = fmaf(s.Q[m * ld + 4 * tx + j], hdo[i][j], x);
-                    x = fmaf(-k, hy[i][j], x);
-                    y = fmaf(k, du1[i][j], y);
-                    hdo[i][j] *= s.g.gam[m];
-                    hy[i][j] = s.g.e[m] * du1[i][j] - s.g.gam[m] * hy[i][j];
-                }
+            for (int n = 0; n < 2; ++n) {
+                const int nb = 32 * wn + 16 * n;
+                if (nb > 16 * wm) continue;
+                uint32_t b[NI][4];
 #pragma unroll
-                for (int o = TX / 2; o; o >>= 1) {
-                    x += __shfl_xor_sync(0xffffffffu, x, o);
-                    y += __shfl_xor_sync(0xffffffffu, y, o);
+                for (int x = 0; x < NI; ++x) frag_b<DK * 2>(b[x], aK + x * (int)U::kKey, k, nb);
+                mma_terms(kk[2 * n], kk[2 * n + 1], ka, b);
+                mma_terms(qk[2 * n], qk[2 * n + 1], qa, b);
+            }
+        }
+        __syncthreads();               // the walk's planes are done with: E, F, M take their place
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int i = 16 * wm + g + 8 * h, j = 32 * wn + 8 * n + q2;
+                float x[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float d = j + c <= i ? exp2f((float)(s.g.G[i] - s.g.G[j + c])) : 0.f;
+                    const float f = j + c < i ? -d * dx[n][2 * h + c] : 0.f;
+                    x[c] = d * dp[n][2 * h + c];
+                    s.tail.F[i * kLdT + j + c] = f;
+                    s.tail.M[i * (kC + 1) + j + c] = j + c < i ? f * kk[n][2 * h + c] + x[c] * qk[n][2 * h + c] : 0.f;
                 }
-                if (tx == 0) {
-                    s.m0[m] = s.g.gam[m] * x;
-                    s.m1[m] = s.g.e[m] * y;
-                }
+                uint32_t u[NE];
+                split2<NE>(x[0], x[1], u);
+#pragma unroll
+                for (int z = 0; z < NE; ++z)
+                    *reinterpret_cast<uint32_t *>(s.tail.E + z * kTri + sw<128>(i, j >> 3) + (j & 7) * 2) = u[z];
+            }
+        // m0_i = gam_i (q_i . H0 dO_i - k_i . H0 Y_i), m1_i = e_i k_i . dH1 U_i: this warp's half of dk
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = 16 * wm + g + 8 * h;
+            const float gam = s.g.gam[i], e = s.g.e[i];
+            float x = 0.f, y = 0.f;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int j = wn * (DK / 2) + 8 * n + q2;
+                const float2 k = pair_at<NI, DK * 2>(s.K, (int)U::kKey, i, j), q = pair_at<NI, DK * 2>(s.Q, (int)U::kKey, i, j);
+                float *a = &hdo[n][2 * h], *b = &hy[n][2 * h], *c = &du[n][2 * h];
+                x = fmaf(q.x, a[0], fmaf(q.y, a[1], fmaf(-k.x, b[0], fmaf(-k.y, b[1], x))));
+                y = fmaf(k.x, c[0], fmaf(k.y, c[1], y));
+                a[0] *= gam;
+                a[1] *= gam;
+                b[0] = e * c[0] - gam * b[0];
+                b[1] = e * c[1] - gam * b[1];
+            }
+            x += __shfl_xor_sync(0xffffffffu, x, 1);
+            x += __shfl_xor_sync(0xffffffffu, x, 2);
+            y += __shfl_xor_sync(0xffffffffu, y, 1);
+            y += __shfl_xor_sync(0xffffffffu, y, 2);
+            if ((lane & 3) == 0) {
+                s.m0[wn][i] = gam * x;
+                s.m1[wn][i] = e * y;
             }
         }
         __syncthreads();
-        gemm<kC, DK, false>(hdo, sE, kLdC, s.K, ld, kC);
-        gemm<kC, DK, true>(hy, sE, kLdC, s.Q, ld, kC);
-        gemm<kC, DK, false>(hy, sF, kLdC, s.K, ld, kC);
-        gemm<kC, DK, true>(hy, sF, kLdC, s.K, ld, kC);
-        each<kC, DK>(hdo, [&](int i, int j, float x) {
-            if (i < t.n) s.dq[(t.tok(i) - t.c * kC) * ld + j] += x;
-        });
-        each<kC, DK>(hy, [&](int i, int j, float x) {
-            if (i < t.n) s.dk[(t.tok(i) - t.c * kC) * ld + j] += x;
-        });
-        // prefix sums along j from the entry, one thread per row; then sums over the rows i >= t
-        if (threadIdx.x < kC) {
-            const int i = threadIdx.x;
-            float x = s.m0[i];
-            for (int j = 0; j < i; ++j) {
-                const float y = sM[i * (kC + 1) + j];
-                sM[i * (kC + 1) + j] = x;      // the sum over columns before token j (0-based)
-                x += y;
-            }
-            sM[i * (kC + 1) + i] = x;
+        for (int e = tid; e < kC * kC / 2; e += kGradThreads) {   // S = F + F^T
+            const int i = e / (kC / 2), j = 2 * (e % (kC / 2));
+            uint32_t u[NE];
+            split2<NE>(s.tail.F[i * kLdT + j] + s.tail.F[j * kLdT + i], s.tail.F[i * kLdT + j + 1] + s.tail.F[(j + 1) * kLdT + i], u);
+#pragma unroll
+            for (int z = 0; z < NE; ++z)
+                *reinterpret_cast<uint32_t *>(s.tail.S + z * kTri + sw<128>(i, j >> 3) + (j & 7) * 2) = u[z];
         }
+        // sums of M over the rows i >= t of their sums over the columns before t; the lane has t = 2 lane, 2 lane + 1.
+        // Row 64 is the chunk's end.
+        float col[2] = {};
+        for (int i = warp; i <= kC; i += 8) {
+            float x, y, from;
+            if (i < kC) {
+                x = s.tail.M[i * (kC + 1) + 2 * lane];
+                y = s.tail.M[i * (kC + 1) + 2 * lane + 1];
+                from = s.m0[0][i] + s.m0[1][i];
+            } else {
+                x = s.m1[0][2 * lane] + s.m1[1][2 * lane];
+                y = s.m1[0][2 * lane + 1] + s.m1[1][2 * lane + 1];
+                from = 0.f;
+#pragma unroll
+                for (int w = 0; w < 8; ++w) from += s.hh[w];
+                from *= s.g.gam[kC - 1];
+            }
+            float sum = x + y;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const float z = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += z;
+            }
+            float before = __shfl_up_sync(0xffffffffu, sum, 1);
+            before = (lane ? before : 0.f) + from;
+            if (i >= 2 * lane) col[0] += before;
+            if (i >= 2 * lane + 1) col[1] += before + x;
+        }
+        s.col[warp][2 * lane] = col[0];
+        s.col[warp][2 * lane + 1] = col[1];
         __syncthreads();
-        if (threadIdx.x < kC) {
-            const int u = threadIdx.x;
-            float x = 0.f;
-            for (int w = 0; w < kThreads / 32; ++w) x += s.red[w];
-            x *= s.g.gam[kC - 1];
-            for (int j = 0; j < u; ++j) x += s.m1[j];
-            for (int i = kC - 1; i >= u; --i) x += sM[i * (kC + 1) + u];
-            if (u < t.n) {
-                const int at = t.tok(u) - t.c * kC;
-                s.da[1][at] += x / s.g.a[u];
-                s.db[1][at] += s.db[0][u];
+        if (tid < t.n) {
+            float a = 0.f, b = 0.f;
+#pragma unroll
+            for (int w = 0; w < 8; ++w) {
+                a += s.col[w][tid];
+                b += s.dbw[w][tid];
+            }
+            const int at = t.tok(tid) - t.c * kC;
+            s.da[at] += a / s.g.a[tid];
+            s.db[at] += b;
+        }
+        // dQ = gam hdo + E K;  dK = e du - gam hy + S K + E^T Q
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint32_t a[NE][4], b[NI][4];
+#pragma unroll
+            for (int n = 0; n < NT / 2; ++n) {
+                const int nb = wn * (DK / 2) + 16 * n;
+#pragma unroll
+                for (int x = 0; x < NI; ++x) frag_bt<DK * 2>(b[x], aK + x * (int)U::kKey, 16 * k, nb);
+                if (k <= wm) {
+#pragma unroll
+                    for (int x = 0; x < NE; ++x) frag_a<128>(a[x], aE + x * kTri, 16 * wm, 16 * k);
+                    mma_terms(hdo[2 * n], hdo[2 * n + 1], a, b);
+                }
+#pragma unroll
+                for (int x = 0; x < NE; ++x) frag_a<128>(a[x], aS + x * kTri, 16 * wm, 16 * k);
+                mma_terms(hy[2 * n], hy[2 * n + 1], a, b);
+                if (k >= wm) {
+#pragma unroll
+                    for (int x = 0; x < NI; ++x) frag_bt<DK * 2>(b[x], aQ + x * (int)U::kKey, 16 * k, nb);
+#pragma unroll
+                    for (int x = 0; x < NE; ++x) frag_at<128>(a[x], aE + x * kTri, 16 * wm, 16 * k);
+                    mma_terms(hy[2 * n], hy[2 * n + 1], a, b);
+                }
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int i = 16 * wm + g + 8 * h;
+            if (i >= t.n) continue;
+            const int tok = t.tok(i), at = tok - t.c * kC;
+            const size_t row = ((size_t)t.head * p.T + tok) * p.dk;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int j = wn * (DK / 2) + 8 * n + q2;
+                if (j >= p.dk) continue;
+                float2 x = make_float2(hdo[n][2 * h], hdo[n][2 * h + 1]), y = make_float2(hy[n][2 * h], hy[n][2 * h + 1]);
+                float2 *px = reinterpret_cast<float2 *>(part + at * DK + j), *py = reinterpret_cast<float2 *>(part + (kC + at) * DK + j);
+                if (!last) {
+                    __stcg(px, x);
+                    __stcg(py, y);
+                    continue;
+                }
+                if (dir == 1) {
+                    const float2 u = __ldcg(px), v = __ldcg(py);
+                    x.x += u.x; x.y += u.y;
+                    y.x += v.x; y.y += v.y;
+                }
+                st2(static_cast<T *>(p.dq) + row + j, x.x, x.y);
+                st2(static_cast<T *>(p.dk_) + row + j, y.x, y.y);
             }
         }
     }
     __syncthreads();
-    const int head = p.head0 + blockIdx.y, base = blockIdx.x * kC, n = min(kC, p.T - base);
-    for (int e = threadIdx.x; e < n * p.dk; e += kThreads) {
-        const int i = e / p.dk, j = e % p.dk;
-        const size_t at = ((size_t)head * p.T + base + i) * p.dk + j;
-        stf(static_cast<T *>(p.dq) + at, s.dq[i * ld + j]);
-        stf(static_cast<T *>(p.dk_) + at, s.dk[i * ld + j]);
-    }
-    if (threadIdx.x < n) {
-        const size_t at = (size_t)head * p.T + base + threadIdx.x;
-        p.dbeta[at] = s.db[1][threadIdx.x];
-        p.ddecay[at] = s.da[1][threadIdx.x];
+    const int base = blockIdx.x * kC, n = min(kC, p.T - base);
+    if (tid < n) {
+        const size_t at = (size_t)(p.head0 + blockIdx.y) * p.T + base + tid;
+        p.dbeta[at] = s.db[tid];
+        p.ddecay[at] = s.da[tid];
     }
 }
 
+// ---------------------------------------------------------------- launches
 template <typename F>
-cudaError_t launch(F kernel, dim3 grid, size_t smem, const BwdParams &p, cudaStream_t stream)
+cudaError_t launch(F kernel, dim3 grid, int threads, size_t smem, const BwdParams &p, cudaStream_t stream)
 {
     cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (err != cudaSuccess) return err;
-    kernel<<<grid, kThreads, smem, stream>>>(p);
+    kernel<<<grid, threads, smem, stream>>>(p);
     err = cudaGetLastError();
     if (err == cudaSuccess) count_launches(1);
     return err;
 }
 
-template <int DK, typename T>
-cudaError_t run(const BwdParams &p, cudaStream_t stream)
-{
-    cudaError_t err = launch(bwd_prepare_kernel<DK, T>, dim3(p.nc, p.heads, p.dirs), sizeof(PrepSmem<DK>), p, stream);
-    if (err == cudaSuccess)
-        err = launch(bwd_chain_kernel<DK, T>, dim3(p.dv / kSl, p.heads, 2 * p.dirs), sizeof(ChainSmem<DK>), p, stream);
-    if (err == cudaSuccess) err = launch(bwd_grad_kernel<DK, T>, dim3(p.nc, p.heads), sizeof(GradSmem<DK>), p, stream);
-    return err;
-}
-
-// The workspace holds both chains' states of every chunk of the heads that one pass takes; passes are cut so
-// that it stays under this, unless one head alone needs more.
+// The workspace holds the operands and both chains' states of every chunk of the heads that one pass takes; passes are
+// cut so that it stays under this, unless one head alone needs more.
 constexpr size_t kMaxWorkspace = (size_t)6 << 30;
 
-}  // namespace
-
-cudaError_t launch_backward(const BwdArgs &a, cudaStream_t stream)
+template <int DK, int NI, typename T>
+cudaError_t run(BwdParams p, cudaStream_t stream)
 {
-    BwdParams p;
-    p.q = a.f.q; p.k = a.f.k; p.v = a.f.v; p.dout = a.dout;
-    p.beta = a.f.beta; p.decay = a.f.decay; p.state_in = a.f.state_in; p.dstate = a.dstate;
-    p.dq = a.dq; p.dk_ = a.dk; p.dv_ = a.dv; p.dbeta = a.dbeta; p.ddecay = a.ddecay; p.dstate_in = a.dstate_in;
-    p.BH = a.f.B * a.f.H; p.T = a.f.T; p.nc = (a.f.T + kC - 1) / kC; p.dk = a.f.dk; p.dv = a.f.dv;
-    p.dirs = a.f.bidi ? 2 : 1;
-    const size_t sq = kC * kC, st = (size_t)p.dk * p.dv, rows = (size_t)kC * p.dv;
-    const size_t per_head = (3 * sq + 2 * st + 2 * rows) * p.nc * p.dirs * sizeof(float);
+    using U = Unit<DK, NI>;
+    using Fwd = Stage<DK, NI, T, 0>;
+    using Bwd = Stage<DK, NI, T, 1>;
+    static_assert(sizeof(GradSmem<DK, NI>) <= 227 * 1024 && sizeof(PrepSmem<DK, NI>) <= 227 * 1024, "shared memory");
+    constexpr size_t chain_smem = std::max((size_t)Fwd::buffers * Fwd::size, (size_t)Bwd::buffers * Bwd::size);
+    static_assert(chain_smem <= 227 * 1024, "shared memory");
+    p.slices = (p.dv + kSlice - 1) / kSlice;
+    const size_t vt = (size_t)p.slices * kC * kSlice * sizeof(T), ot = (size_t)p.slices * NI * kC * 128;
+    const size_t state = (size_t)p.dv * DK * sizeof(float), rows = (size_t)p.dv * kC * sizeof(float);
+    const size_t per_head = (U::size + vt + ot + 2 * state + 2 * rows) * p.nc * p.dirs;
     const int most = (int)std::min<size_t>((size_t)p.BH, std::max<size_t>(1, kMaxWorkspace / per_head));
     const int passes = (p.BH + most - 1) / most, each_pass = (p.BH + passes - 1) / passes;
-    float *ws = nullptr;
+    unsigned char *ws = nullptr;
     cudaError_t err = ws_alloc(reinterpret_cast<void **>(&ws), per_head * each_pass, stream);
     if (err != cudaSuccess) return err;
     for (int h = 0; h < p.BH && err == cudaSuccess; h += each_pass) {
         p.head0 = h;
         p.heads = std::min(each_pass, p.BH - h);
         const size_t n = (size_t)p.nc * p.dirs * p.heads;
-        p.X = ws;
-        p.P = p.X + n * sq;
-        p.N = p.P + n * sq;
-        p.H0 = p.N + n * sq;
-        p.dH1 = p.H0 + n * st;
-        p.W = p.dH1 + n * st;
-        p.Z = p.W + n * rows;
-        if (a.f.fp32) err = p.dk <= 64 ? run<64, float>(p, stream) : run<128, float>(p, stream);
-        else err = p.dk <= 64 ? run<64, __nv_bfloat16>(p, stream) : run<128, __nv_bfloat16>(p, stream);
+        p.unit = ws;
+        p.vt = p.unit + n * U::size;
+        p.ot = p.vt + n * vt;
+        p.HT = reinterpret_cast<float *>(p.ot + n * ot);
+        p.GT = p.HT + n * p.dv * DK;
+        p.WT = p.GT + n * p.dv * DK;
+        p.ZT = p.WT + n * p.dv * kC;
+        err = launch(bwd_prepare_kernel<DK, NI, T>, dim3(p.nc, p.heads, p.dirs), kPrepThreads, sizeof(PrepSmem<DK, NI>), p, stream);
+        if (err == cudaSuccess)
+            err = launch(bwd_chain_kernel<DK, NI, T>, dim3(p.slices, p.heads, 2 * p.dirs), kChainThreads, chain_smem, p, stream);
+        if (err == cudaSuccess)
+            err = launch(bwd_grad_kernel<DK, NI, T>, dim3(p.nc, p.heads), kGradThreads, sizeof(GradSmem<DK, NI>), p, stream);
     }
     const cudaError_t e2 = ws_free(ws, stream);
     return err != cudaSuccess ? err : e2;
+}
+
+}  // namespace
+
+cudaError_t launch_backward(const BwdArgs &a, cudaStream_t stream)
+{
+    BwdParams p = {};
+    p.q = a.f.q; p.k = a.f.k; p.v = a.f.v; p.dout = a.dout;
+    p.beta = a.f.beta; p.decay = a.f.decay; p.state_in = a.f.state_in; p.dstate = a.dstate;
+    p.dq = a.dq; p.dk_ = a.dk; p.dv_ = a.dv; p.dbeta = a.dbeta; p.ddecay = a.ddecay; p.dstate_in = a.dstate_in;
+    p.BH = a.f.B * a.f.H; p.T = a.f.T; p.nc = (a.f.T + kC - 1) / kC; p.dk = a.f.dk; p.dv = a.f.dv;
+    p.dirs = a.f.bidi ? 2 : 1;
+    if (a.f.fp32) return p.dk <= 64 ? run<64, 3, float>(p, stream) : run<128, 3, float>(p, stream);
+    return p.dk <= 64 ? run<64, 1, __nv_bfloat16>(p, stream) : run<128, 1, __nv_bfloat16>(p, stream);
 }
 
 }  // namespace gdn
