@@ -51,7 +51,7 @@ namespace gdn {
 namespace {
 
 constexpr int kC = 64;             // tokens per chunk
-constexpr int kSlice = 64;         // dv columns per chain block and per V / dO tile
+constexpr int kSlice = 32;         // dv columns of a V or dO tile
 constexpr int kTri = kC * kC * 2;  // bytes of one term plane of N or P
 
 __device__ __forceinline__ float ldf(const float *p) { return *p; }
@@ -71,7 +71,7 @@ struct Gates {
 };
 
 // Workspace of one (direction, head, chunk), in bytes.  Tiles are row-major with the 16-byte pieces of a
-// row XOR-ed by row % 8, so that eight rows' pieces of one column lie in eight bank groups.
+// row XOR-ed by the row's number, so that eight rows' pieces of one column lie in eight bank groups.
 template <int DK, int NI>
 struct Unit {
     static constexpr size_t kKey = (size_t)kC * DK * 2;    // one term plane of K or Q
@@ -91,8 +91,8 @@ struct BwdParams {
     float *dbeta, *ddecay, *dstate_in;
     // workspace of this launch's heads, one entry per (direction, head, chunk)
     unsigned char *unit;       // Unit<DK, NI>
-    unsigned char *vt;         // [slice][64 tokens][64 columns] of the input type
-    unsigned char *ot;         // [slice][NI planes][64 tokens][64 columns]
+    unsigned char *vt;         // [slice][64 tokens][32 columns] of the input type
+    unsigned char *ot;         // [slice][NI planes][64 tokens][32 columns]
     float *HT, *GT;            // [dv][DK]: H0 and dH1, transposed
     float *WT, *ZT;            // [dv][64 tokens]
     int head0, heads;          // the heads [head0, head0 + heads) of B*H
@@ -139,7 +139,10 @@ __device__ __forceinline__ float hi16(uint32_t u) { return __uint_as_float(u & 0
 
 // byte offset of the 16-byte piece `piece` of row `row` in a swizzled tile with RB-byte rows
 template <int RB>
-__device__ __forceinline__ uint32_t sw(int row, int piece) { return row * RB + ((piece ^ (row & 7)) << 4); }
+__device__ __forceinline__ uint32_t sw(int row, int piece)
+{
+    return row * RB + ((piece ^ (RB == 64 ? (row >> 1) & 3 : row & 7)) << 4);
+}
 
 __device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr)
 {
@@ -187,27 +190,35 @@ __device__ __forceinline__ void frag_bt(uint32_t (&r)[4], uint32_t tile, int k, 
     ldsm_t(r, tile + sw<RB>(k + (l & 15), (n >> 3) + (l >> 4)));
 }
 
-// c (m16 x n16, two n8 tiles) += A B over the terms: products of order i + j < 3 (one term each: 0), the small ones
-// first and all into a sum of their own, which an ordinary addition, rounded to nearest, adds to c: the truncation of
-// the tensor core's sums then touches every 16 products once and does not pile up over k.
-template <int NA, int NB>
-__device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4])
+// c (m16 x n16, two n8 tiles) += the sum of KS products A B over the terms: products of order i + j < 3 (one term
+// each: 0), the small ones first and all into a sum of their own, which an ordinary addition, rounded to nearest, adds to
+// c: the truncation of the tensor core's sums then touches every 16 KS products once and does not pile up over k.
+template <int KS, int NA, int NB>
+__device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[KS][NA][4], const uint32_t (&b)[KS][NB][4])
 {
     float d0[4] = {}, d1[4] = {};
 #pragma unroll
     for (int order = NA + NB - 2 < 2 ? NA + NB - 2 : 2; order >= 0; --order)
 #pragma unroll
-        for (int i = 0; i < NA; ++i) {
-            const int j = order - i;
-            if (j < 0 || j >= NB) continue;
-            mma(d0, a[i], b[j][0], b[j][1]);
-            mma(d1, a[i], b[j][2], b[j][3]);
-        }
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int i = 0; i < NA; ++i) {
+                const int j = order - i;
+                if (j < 0 || j >= NB) continue;
+                mma(d0, a[k][i], b[k][j][0], b[k][j][1]);
+                mma(d1, a[k][i], b[k][j][2], b[k][j][3]);
+            }
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
         c0[x] += d0[x];
         c1[x] += d1[x];
     }
+}
+
+template <int NA, int NB>
+__device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4])
+{
+    mma_terms<1, NA, NB>(c0, c1, reinterpret_cast<const uint32_t (&)[1][NA][4]>(a), reinterpret_cast<const uint32_t (&)[1][NB][4]>(b));
 }
 
 // the left operand whose columns k .. k + 15 are the accumulator tiles x, y times per-column factors
@@ -255,8 +266,6 @@ template <int DK, int NI>
 struct PrepSmem {
     unsigned char K[NI * Unit<DK, NI>::kKey];
     unsigned char Q[NI * Unit<DK, NI>::kKey];
-    unsigned char Np[3 * kTri];
-    unsigned char Pp[3 * kTri];
     float X[kC * (kC + 4)];        // X diag(b)
     float N[kC * (kC + 4)];
     Gates g;
@@ -361,20 +370,20 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
     }
     const T *vb = static_cast<const T *>(p.v) + (size_t)t.head * p.T * p.dv;
     const T *ob = static_cast<const T *>(p.dout) + (size_t)t.head * p.T * p.dv;
-    for (int e = tid; e < p.slices * kC * 8; e += kPrepThreads) {
-        const int sl = e / (kC * 8), i = e / 8 % kC, c = e % 8;
+    for (int e = tid; e < p.slices * kC * 4; e += kPrepThreads) {
+        const int sl = e / (kC * 4), i = e / 4 % kC, c = e % 4;
         const bool on = i < t.n;
         const size_t row = on ? (size_t)t.tok(i) * p.dv : 0;
         float x[8];
         get8(ob + row, on, sl * kSlice + 8 * c, p.dv, x);
-        put8<NI, 128, T>(x, i, c, nullptr, p.ot + (t.ws * p.slices + sl) * (NI * kC * 128), kC * 128);
+        put8<NI, 64, T>(x, i, c, nullptr, p.ot + (t.ws * p.slices + sl) * (NI * kC * 64), kC * 64);
         get8(vb + row, on, sl * kSlice + 8 * c, p.dv, x);
         unsigned char *vt = p.vt + (t.ws * p.slices + sl) * (kC * kSlice * sizeof(T));
         if constexpr (sizeof(T) == 2) {
-            put8<1, 128, T>(x, i, c, nullptr, vt, 0);
+            put8<1, 64, T>(x, i, c, nullptr, vt, 0);
         } else {
-            *reinterpret_cast<float4 *>(vt + sw<256>(i, 2 * c)) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4 *>(vt + sw<256>(i, 2 * c + 1)) = make_float4(x[4], x[5], x[6], x[7]);
+            *reinterpret_cast<float4 *>(vt + sw<128>(i, 2 * c)) = make_float4(x[0], x[1], x[2], x[3]);
+            *reinterpret_cast<float4 *>(vt + sw<128>(i, 2 * c + 1)) = make_float4(x[4], x[5], x[6], x[7]);
         }
     }
     __syncthreads();
@@ -422,7 +431,7 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
             split2<3>(y[0], y[1], u);
 #pragma unroll
             for (int x3 = 0; x3 < 3; ++x3)
-                *reinterpret_cast<uint32_t *>(s.Pp + x3 * kTri + sw<128>(i, j >> 3) + (j & 7) * 2) = u[x3];
+                *reinterpret_cast<uint32_t *>(unit + U::P + x3 * kTri + sw<128>(i, j >> 3) + (j & 7) * 2) = u[x3];
         }
     __syncthreads();
     // N <- X - (X diag(b)) N in block rows of 16: the rows above by all threads, the 16 x 16 triangle by one
@@ -459,98 +468,118 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
         }
         __syncthreads();
     }
-    for (int e = tid; e < kC * kC / 2; e += kPrepThreads) {
-        const int i = e / (kC / 2), j = 2 * (e % (kC / 2));
-        uint32_t u[3];
-        split2<3>(s.N[i * ld + j], s.N[i * ld + j + 1], u);
+    for (int e = tid; e < kC * kC / 8; e += kPrepThreads) {
+        const int i = e / (kC / 8), c = e % (kC / 8);
+        float x[8];
 #pragma unroll
-        for (int x = 0; x < 3; ++x)
-            *reinterpret_cast<uint32_t *>(s.Np + x * kTri + sw<128>(i, j >> 3) + (j & 7) * 2) = u[x];
-    }
-    __syncthreads();
-    for (int o = tid * 16; o < 3 * kTri; o += kPrepThreads * 16) {
-        *reinterpret_cast<uint4 *>(unit + U::N + o) = *reinterpret_cast<const uint4 *>(s.Np + o);
-        *reinterpret_cast<uint4 *>(unit + U::P + o) = *reinterpret_cast<const uint4 *>(s.Pp + o);
+        for (int u = 0; u < 8; ++u) x[u] = s.N[i * ld + 8 * c + u];
+        put8<3, 128, T>(x, i, c, nullptr, unit + U::N, kTri);
     }
 }
 
 // ---------------------------------------------------------------- chains
-// Grid (slices of 64 columns, heads, direction and walk), four warps of 16 columns each.
-constexpr int kChainThreads = 128;
+// Grid (groups of 16 PAIRS columns of dv, heads, directions and walks).  A pair of warps carries 16 columns: each holds
+// half of dk of H^T, their partial H^T K^T meet in shared memory, and both go on with the whole of W (or Z), the
+// triangular product being the only one that is done twice.  One warp per 16 columns would spare that, but takes
+// 8.9 us for a chunk of 64 tokens (dk = dv = 128, bf16): a walk is bound by its own latency, and the pair shortens it.
 
-// bytes of one stage: the unit's tiles from its start (forward: gates, N, K; backward: all) and the slice's V or dO
-template <int DK, int NI, typename T, int WALK>
+// bytes of one stage: the unit's tiles from its start (forward: gates, N, K; backward: all) and V or dO
+template <int DK, int NI, typename T, int WALK, int PAIRS>
 struct Stage {
     using U = Unit<DK, NI>;
     static constexpr int head = WALK ? (int)U::size : (int)U::Q;
-    static constexpr int tile = WALK ? NI * kC * 128 : kC * kSlice * (int)sizeof(T);
-    static constexpr int size = head + tile;
-    static constexpr int buffers = 2 * size <= 227 * 1024 ? 2 : 1;
+    static constexpr int tile = WALK ? NI * kC * 64 : kC * kSlice * (int)sizeof(T);
+    static constexpr int size = head + PAIRS / 2 * tile;
+    static constexpr int meet = PAIRS * 2 * 8 * 32 * 16;       // the pairs' partial products
+    static constexpr int buffers = meet + 2 * size <= 227 * 1024 ? 2 : 1;
+    static constexpr int bytes = meet + buffers * size;
 };
 
-// r (16 x 64, columns tokens) += h^T-fragments times K^T
-template <int DK, int NI>
-__device__ __forceinline__ void state_times_keys(float (&r)[8][4], const float (&h)[DK / 8][4], uint32_t K)
-{
-    const float one[4] = {1.f, 1.f, 1.f, 1.f};
-#pragma unroll
-    for (int k = 0; k < DK / 16; ++k) {
-        uint32_t a[3][4];
-        acc_to_a<3>(a, h[2 * k], h[2 * k + 1], one);
-#pragma unroll
-        for (int n = 0; n < 4; ++n) {
-            uint32_t b[NI][4];
-#pragma unroll
-            for (int x = 0; x < NI; ++x) frag_b<DK * 2>(b[x], K + x * (int)Unit<DK, NI>::kKey, 16 * k, 16 * n);
-            mma_terms(r[2 * n], r[2 * n + 1], a, b);
-        }
-    }
-}
-
-// h (16 x dk) += A X, A the 16 x 16 left operand of tokens 16 k .. (terms), X the tile K or Q
-template <int DK, int NI, int NA>
-__device__ __forceinline__ void add_outer(float (&h)[DK / 8][4], const uint32_t (&a)[NA][4], uint32_t X, int k)
-{
-#pragma unroll
-    for (int n = 0; n < DK / 16; ++n) {
-        uint32_t b[NI][4];
-#pragma unroll
-        for (int x = 0; x < NI; ++x) frag_bt<DK * 2>(b[x], X + x * (int)Unit<DK, NI>::kKey, 16 * k, 16 * n);
-        mma_terms(h[2 * n], h[2 * n + 1], a, b);
-    }
-}
-
-template <int DK, int NI, typename T, int WALK>
+template <int DK, int NI, typename T, int WALK, int PAIRS>
 __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char *raw)
 {
     using U = Unit<DK, NI>;
-    using S = Stage<DK, NI, T, WALK>;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q2 = 2 * (lane & 3);
-    const int local = blockIdx.y, head = p.head0 + local, sl = blockIdx.x;
-    const int row = sl * kSlice + 16 * warp;                   // this warp's columns of dv: rows of H^T
+    using S = Stage<DK, NI, T, WALK, PAIRS>;
+    constexpr int HK = DK / 2, NT = HK / 8, KP = (int)U::kKey; // a warp's half of dk, its n8 tiles, a plane of K
+    const int lane = threadIdx.x & 31, half = (threadIdx.x >> 5) & 1, pair = threadIdx.x >> 6;
+    const int g = lane >> 2, q2 = 2 * (lane & 3), k0 = half * HK;
+    const int local = blockIdx.y, head = p.head0 + local, sl = blockIdx.x * (PAIRS / 2);
+    const int row = 16 * (blockIdx.x * PAIRS + pair);          // this pair's columns of dv: rows of H^T
     const bool on = row < p.dv;
+    const int tiles = min(PAIRS / 2, p.slices - sl) * S::tile;
     const size_t st = (size_t)p.dk * p.dv;
-    float h[DK / 8][4];
+    float h[NT][4];
     const float *init = nullptr;
     if (WALK == 0 && dir == 0 && p.state_in) init = p.state_in + head * st;
     if (WALK == 1 && p.dstate) init = p.dstate + ((size_t)dir * p.BH + head) * st;
 #pragma unroll
-    for (int n = 0; n < DK / 8; ++n)
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-            const int kx = 8 * n + q2 + (x & 1), vx = row + g + 8 * (x >> 1);
+            const int kx = k0 + 8 * n + q2 + (x & 1), vx = row + g + 8 * (x >> 1);
             h[n][x] = init && on && kx < p.dk ? init[(size_t)kx * p.dv + vx] : 0.f;
         }
 
-    const uint32_t base = ptx::smem_u32(raw);
+    float4 *const mine = reinterpret_cast<float4 *>(raw) + (pair * 2 + half) * 256 + lane;
+    const float4 *const other = reinterpret_cast<const float4 *>(raw) + (pair * 2 + 1 - half) * 256 + lane;
+    unsigned char *const stages = raw + S::meet;
+    const uint32_t base = ptx::smem_u32(stages);
     auto fetch = [&](int step) {
         const int c = (dir ^ WALK) ? p.nc - 1 - step : step;
         const size_t ws = ((size_t)dir * p.heads + local) * p.nc + c;
         const uint32_t dst = base + (step % S::buffers) * S::size;
         copy_block(dst, p.unit + ws * U::size, S::head);
-        copy_block(dst + S::head, (WALK ? p.ot : p.vt) + (ws * p.slices + sl) * S::tile, S::tile);
+        copy_block(dst + S::head, (WALK ? p.ot : p.vt) + (ws * p.slices + sl) * S::tile, tiles);
         copy_commit();
     };
+    // r (16 x 64, columns tokens) += the warp's part of H^T K^T
+    auto state_times_keys = [&](float (&r)[8][4], uint32_t tK) {
+        const float one[4] = {1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+        for (int k = 0; k < HK / 16; k += 2) {
+            uint32_t a[2][3][4];
+            acc_to_a<3>(a[0], h[2 * k], h[2 * k + 1], one);
+            acc_to_a<3>(a[1], h[2 * k + 2], h[2 * k + 3], one);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                uint32_t b[2][NI][4];
+#pragma unroll
+                for (int x = 0; x < NI; ++x) {
+                    frag_b<DK * 2>(b[0][x], tK + x * KP, k0 + 16 * k, 16 * n);
+                    frag_b<DK * 2>(b[1][x], tK + x * KP, k0 + 16 * k + 16, 16 * n);
+                }
+                mma_terms<2, 3, NI>(r[2 * n], r[2 * n + 1], a, b);
+            }
+        }
+    };
+    // h += A X: A the left operands of tokens 16 k .. 16 k + 31, X the tile K or Q
+    auto add_outer = [&](const uint32_t (&a)[2][3][4], uint32_t tX, int k) {
+#pragma unroll
+        for (int n = 0; n < HK / 16; ++n) {
+            uint32_t b[2][NI][4];
+#pragma unroll
+            for (int x = 0; x < NI; ++x) {
+                frag_bt<DK * 2>(b[0][x], tX + x * KP, 16 * k, k0 + 16 * n);
+                frag_bt<DK * 2>(b[1][x], tX + x * KP, 16 * k + 16, k0 + 16 * n);
+            }
+            mma_terms<2, 3, NI>(h[2 * n], h[2 * n + 1], a, b);
+        }
+    };
+    // adds the other warp's part of r to this one's
+    auto meet = [&](float (&r)[8][4]) {
+#pragma unroll
+        for (int n = 0; n < 8; ++n) mine[32 * n] = make_float4(r[n][0], r[n][1], r[n][2], r[n][3]);
+        asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
+#pragma unroll
+        for (int n = 0; n < 8; ++n) {
+            const float4 y = other[32 * n];
+            r[n][0] += y.x;
+            r[n][1] += y.y;
+            r[n][2] += y.z;
+            r[n][3] += y.w;
+        }
+    };
+
     if (S::buffers == 2) fetch(0);
     for (int step = 0; step < p.nc; ++step) {
         const int c = (dir ^ WALK) ? p.nc - 1 - step : step;
@@ -564,32 +593,37 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
         if (S::buffers == 2 && step + 1 < p.nc) fetch(step + 1);   // into the stage that all warps have left
         if (!on) continue;
         const int so = (step % S::buffers) * S::size;
-        const Gates &gt = *reinterpret_cast<const Gates *>(raw + so);
-        const uint32_t tN = base + so + (uint32_t)U::N, tK = base + so + (uint32_t)U::K, tX = base + so + S::head;
+        const Gates &gt = *reinterpret_cast<const Gates *>(stages + so);
+        const uint32_t tN = base + so + (uint32_t)U::N, tK = base + so + (uint32_t)U::K;
         {
-            float *keep = (WALK ? p.GT : p.HT) + (ws * p.dv + row) * DK;
+            float *keep = (WALK ? p.GT : p.HT) + (ws * p.dv + row) * DK + k0;
 #pragma unroll
-            for (int n = 0; n < DK / 8; ++n) {
+            for (int n = 0; n < NT; ++n) {
                 st2(keep + (size_t)g * DK + 8 * n + q2, h[n][0], h[n][1]);
                 st2(keep + (size_t)(g + 8) * DK + 8 * n + q2, h[n][2], h[n][3]);
             }
         }
         float r[8][4] = {}, w[8][4];
-        state_times_keys<DK, NI>(r, h, tK);
+        state_times_keys(r, tK);
         const float gend = gt.gam[kC - 1];
 #pragma unroll
-        for (int n = 0; n < DK / 8; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int x = 0; x < 4; ++x) h[n][x] *= gend;
-        float *out = (WALK ? p.ZT : p.WT) + (ws * p.dv + row) * kC;
+        // per-token factors at the fragment's columns of tokens 16 k ..
+        auto factors = [&](float (&f)[4], int k, auto of) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) f[x] = of(16 * k + q2 + (x & 1) + 8 * (x >> 1));
+        };
         if (WALK == 0) {
+            meet(r);
             // R = V - gam (H^T K^T)
-            const unsigned char *vt = raw + so + S::head;
+            const unsigned char *vt = stages + so + S::head + (pair >> 1) * S::tile;
 #pragma unroll
             for (int n = 0; n < 8; ++n)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
-                    const int i = 8 * n + q2 + (x & 1), v = 16 * warp + g + 8 * (x >> 1);
+                    const int i = 8 * n + q2 + (x & 1), v = 16 * (pair & 1) + g + 8 * (x >> 1);
                     constexpr int RB = kSlice * sizeof(T), per = 16 / sizeof(T);
                     const float y = ldf(reinterpret_cast<const T *>(vt + sw<RB>(i, v / per)) + v % per);
                     r[n][x] = y - gt.gam[i] * r[n][x];
@@ -599,9 +633,8 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 float f[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) f[x] = -gt.b[16 * k + q2 + (x & 1) + 8 * (x >> 1)];
                 uint32_t a[3][4];
+                factors(f, k, [&](int i) { return -gt.b[i]; });
                 acc_to_a<3>(a, r[2 * k], r[2 * k + 1], f);
 #pragma unroll
                 for (int n = k; n < 4; ++n) {
@@ -611,51 +644,44 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
                     mma_terms(w[2 * n], w[2 * n + 1], a, b);
                 }
             }
-            // H <- gam_C H + K^T diag(e b) W
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float f[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int i = 16 * k + q2 + (x & 1) + 8 * (x >> 1);
-                    f[x] = gt.e[i] * gt.b[i];
-                }
-                uint32_t a[3][4];
-                acc_to_a<3>(a, w[2 * k], w[2 * k + 1], f);
-                add_outer<DK, NI>(h, a, tK, k);
-            }
         } else {
             const uint32_t tQ = base + so + (uint32_t)U::Q, tP = base + so + (uint32_t)U::P;
-            // dU = diag(e) K dH1 + P^T dO: tokens i = 16 k .. feed tokens j <= i; and dH += Q^T diag(gam) dO
+            const uint32_t tX = base + so + S::head + (pair >> 1) * S::tile;
+            // dU = diag(e) K dH1 + P^T dO, tokens i = 16 k .. feeding tokens j <= i: the warps take two k each
 #pragma unroll
             for (int n = 0; n < 8; ++n)
 #pragma unroll
                 for (int x = 0; x < 4; ++x) r[n][x] *= gt.e[8 * n + q2 + (x & 1)];
+            // and dH += Q^T diag(gam) dO
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                uint32_t o[NI][4], a[3][4];
+            for (int k = 0; k < 4; k += 2) {
+                uint32_t a[2][3][4];
 #pragma unroll
-                for (int x = 0; x < NI; ++x) frag_at<128>(o[x], tX + x * (kC * 128), 16 * warp, 16 * k);
+                for (int kk = k; kk < k + 2; ++kk) {
+                    uint32_t o[NI][4];
 #pragma unroll
-                for (int n = 0; n <= k; ++n) {
-                    uint32_t b[3][4];
+                    for (int x = 0; x < NI; ++x) frag_at<64>(o[x], tX + x * (kC * 64), 16 * (pair & 1), 16 * kk);
+                    if ((kk == 0 || kk == 3) == (half == 0)) {
 #pragma unroll
-                    for (int x = 0; x < 3; ++x) frag_bt<128>(b[x], tP + x * kTri, 16 * k, 16 * n);
-                    mma_terms(r[2 * n], r[2 * n + 1], o, b);
+                        for (int n = 0; n <= kk; ++n) {
+                            uint32_t b[3][4];
+#pragma unroll
+                            for (int x = 0; x < 3; ++x) frag_bt<128>(b[x], tP + x * kTri, 16 * kk, 16 * n);
+                            mma_terms(r[2 * n], r[2 * n + 1], o, b);
+                        }
+                    }
+                    float f[4], u[4] = {}, v[4] = {};
+                    factors(f, kk, [&](int i) { return gt.gam[i]; });
+#pragma unroll
+                    for (int x = NI - 1; x >= 0; --x) {
+                        u[0] += lo16(o[x][0]); u[1] += hi16(o[x][0]); u[2] += lo16(o[x][1]); u[3] += hi16(o[x][1]);
+                        v[0] += lo16(o[x][2]); v[1] += hi16(o[x][2]); v[2] += lo16(o[x][3]); v[3] += hi16(o[x][3]);
+                    }
+                    acc_to_a<3>(a[kk - k], u, v, f);
                 }
-                float f[4], u[4], v[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) f[x] = gt.gam[16 * k + q2 + (x & 1) + 8 * (x >> 1)];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) u[x] = v[x] = 0.f;
-#pragma unroll
-                for (int x = NI - 1; x >= 0; --x) {
-                    u[0] += lo16(o[x][0]); u[1] += hi16(o[x][0]); u[2] += lo16(o[x][1]); u[3] += hi16(o[x][1]);
-                    v[0] += lo16(o[x][2]); v[1] += hi16(o[x][2]); v[2] += lo16(o[x][3]); v[3] += hi16(o[x][3]);
-                }
-                acc_to_a<3>(a, u, v, f);
-                add_outer<DK, NI>(h, a, tQ, k);
+                add_outer(a, tQ, k);
             }
+            meet(r);
             // Z = dU - N^T diag(b) dU: tokens i = 16 k .. feed tokens j <= i
 #pragma unroll
             for (int n = 0; n < 8; ++n)
@@ -664,9 +690,8 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
                 float f[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) f[x] = -gt.b[16 * k + q2 + (x & 1) + 8 * (x >> 1)];
                 uint32_t a[3][4];
+                factors(f, k, [&](int i) { return -gt.b[i]; });
                 acc_to_a<3>(a, r[2 * k], r[2 * k + 1], f);
 #pragma unroll
                 for (int n = 0; n <= k; ++n) {
@@ -676,51 +701,52 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
                     mma_terms(w[2 * n], w[2 * n + 1], a, b);
                 }
             }
-            // dH -= K^T diag(gam b) Z
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                float f[4];
-#pragma unroll
-                for (int x = 0; x < 4; ++x) {
-                    const int i = 16 * k + q2 + (x & 1) + 8 * (x >> 1);
-                    f[x] = -gt.gam[i] * gt.b[i];
-                }
-                uint32_t a[3][4];
-                acc_to_a<3>(a, w[2 * k], w[2 * k + 1], f);
-                add_outer<DK, NI>(h, a, tK, k);
-            }
         }
+        float *out = (WALK ? p.ZT : p.WT) + (ws * p.dv + row) * kC;
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
+            if ((n >> 2) != half) continue;
             st2(out + (size_t)g * kC + 8 * n + q2, w[n][0], w[n][1]);
             st2(out + (size_t)(g + 8) * kC + 8 * n + q2, w[n][2], w[n][3]);
+        }
+        // H <- gam_C H + K^T diag(e b) W, or dH <- ... - K^T diag(gam b) Z
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+            uint32_t a[2][3][4];
+#pragma unroll
+            for (int kk = k; kk < k + 2; ++kk) {
+                float f[4];
+                factors(f, kk, [&](int i) { return WALK ? -gt.gam[i] * gt.b[i] : gt.e[i] * gt.b[i]; });
+                acc_to_a<3>(a[kk - k], w[2 * kk], w[2 * kk + 1], f);
+            }
+            add_outer(a, tK, k);
         }
     }
     if (WALK == 1 && dir == 0 && on && p.dstate_in) {
         float *to = p.dstate_in + head * st;
 #pragma unroll
-        for (int n = 0; n < DK / 8; ++n)
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
-                const int kx = 8 * n + q2 + (x & 1), vx = row + g + 8 * (x >> 1);
+                const int kx = k0 + 8 * n + q2 + (x & 1), vx = row + g + 8 * (x >> 1);
                 if (kx < p.dk) to[(size_t)kx * p.dv + vx] = h[n][x];
             }
     }
 }
 
-template <int DK, int NI, typename T>
-__global__ void __launch_bounds__(kChainThreads) bwd_chain_kernel(const __grid_constant__ BwdParams p)
+template <int DK, int NI, typename T, int PAIRS>
+__global__ void __launch_bounds__(64 * PAIRS, 1) bwd_chain_kernel(const __grid_constant__ BwdParams p)
 {
     extern __shared__ __align__(128) unsigned char raw[];
     // the backward walks, the longer ones, come first
-    if (blockIdx.z < p.dirs) chain<DK, NI, T, 1>(p, blockIdx.z, raw);
-    else chain<DK, NI, T, 0>(p, blockIdx.z - p.dirs, raw);
+    if (blockIdx.z < p.dirs) chain<DK, NI, T, 1, PAIRS>(p, blockIdx.z, raw);
+    else chain<DK, NI, T, 0, PAIRS>(p, blockIdx.z - p.dirs, raw);
 }
 
 // ---------------------------------------------------------------- gradients
 // Grid (chunks, heads), eight warps: warp w has the tokens 16 (w % 4) .. of every result and its columns' half w / 4.
 constexpr int kGradThreads = 256;
-constexpr int kStep = 32;              // dv columns per step of the walk over dv
+constexpr int kStep = kSlice;          // dv columns per step of the walk over dv
 constexpr int kLdT = kC + 4;           // pitch of 64-wide fp32 rows
 
 template <int DK, int NI>
@@ -728,7 +754,7 @@ struct GradSmem {
     using U = Unit<DK, NI>;
     static constexpr bool kStage = NI == 1;                    // room for the next step's fp32 tiles
     static constexpr int NE = NI == 1 ? 2 : 3;                 // terms of E and F (results of NI = 1 are bf16)
-    static constexpr int kOTiles = NI == 1 ? 2 : 1;            // dO: every slice, or the walk's
+    static constexpr int kOTiles = NI == 1 ? 4 : 1;            // dO: every slice, or the step's
     static constexpr int kState = kStep * DK * 2, kVal = kStep * kC * 2;
     struct Walk {                                              // term planes of the step's H0, dH1, U, Y: rows dv
         unsigned char H[3 * kState], G[3 * kState], U[3 * kVal], Y[3 * kVal];
@@ -739,7 +765,7 @@ struct GradSmem {
     };
     Gates g;
     unsigned char K[NI * U::kKey], Q[NI * U::kKey];
-    unsigned char O[kOTiles * NI * kC * 128];
+    unsigned char O[kOTiles * NI * kC * 64];
     union {
         Walk walk;
         Tail tail;
@@ -830,14 +856,13 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
             }
             copy_rows(s.Z, kLdT, ZT + (size_t)c0 * kC, kC);
             if (dir == 1) copy_rows(s.Z0, kLdT, ZT0 + (size_t)c0 * kC, kC);
-            if (!Sm::kStage && c0 % kSlice == 0)
-                copy_block(aO, p.ot + (t.ws * p.slices + c0 / kSlice) * (NI * kC * 128), NI * kC * 128);
+            if (!Sm::kStage) copy_block(aO, p.ot + (t.ws * p.slices + c0 / kSlice) * (NI * kC * 64), NI * kC * 64);
             copy_commit();
         };
         copy_block(ptx::smem_u32(&s.g), unit, sizeof(Gates));
         copy_block(aK, unit + U::K, NI * (int)U::kKey);
         copy_block(aQ, unit + U::Q, NI * (int)U::kKey);
-        if (Sm::kStage) copy_block(aO, p.ot + t.ws * p.slices * (NI * kC * 128), p.slices * NI * kC * 128);
+        if (Sm::kStage) copy_block(aO, p.ot + t.ws * p.slices * (NI * kC * 64), p.slices * NI * kC * 64);
         fetch(0);
 
         float hdo[NT][4] = {}, hy[NT][4] = {}, du[NT][4] = {}, dp[4][4] = {}, dx[4][4] = {}, db[8] = {}, hh = 0.f;
@@ -884,9 +909,9 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
 #pragma unroll
             for (int k = 0; k < kStep; k += 16) {
                 uint32_t o[NI][4], u[3][4], y[3][4];
-                const uint32_t ot = aO + (Sm::kStage ? c0 / kSlice : 0) * (NI * kC * 128);
+                const uint32_t ot = aO + (Sm::kStage ? c0 / kSlice : 0) * (NI * kC * 64);
 #pragma unroll
-                for (int x = 0; x < NI; ++x) frag_a<128>(o[x], ot + x * (kC * 128), 16 * wm, c0 % kSlice + k);
+                for (int x = 0; x < NI; ++x) frag_a<64>(o[x], ot + x * (kC * 64), 16 * wm, k);
 #pragma unroll
                 for (int x = 0; x < 3; ++x) {
                     frag_at<128>(u[x], aU + x * Sm::kVal, 16 * wm, k);
@@ -1122,6 +1147,15 @@ cudaError_t launch(F kernel, dim3 grid, int threads, size_t smem, const BwdParam
     return err;
 }
 
+template <int DK, int NI, typename T, int PAIRS>
+cudaError_t launch_chains(const BwdParams &p, cudaStream_t stream)
+{
+    constexpr int smem = std::max(Stage<DK, NI, T, 0, PAIRS>::bytes, Stage<DK, NI, T, 1, PAIRS>::bytes);
+    static_assert(smem <= 227 * 1024, "shared memory");
+    return launch(bwd_chain_kernel<DK, NI, T, PAIRS>, dim3((p.slices + PAIRS / 2 - 1) / (PAIRS / 2), p.heads, 2 * p.dirs), 64 * PAIRS,
+                  smem, p, stream);
+}
+
 // The workspace holds the operands and both chains' states of every chunk of the heads that one pass takes; passes are
 // cut so that it stays under this, unless one head alone needs more.
 constexpr size_t kMaxWorkspace = (size_t)6 << 30;
@@ -1130,24 +1164,25 @@ template <int DK, int NI, typename T>
 cudaError_t run(BwdParams p, cudaStream_t stream)
 {
     using U = Unit<DK, NI>;
-    using Fwd = Stage<DK, NI, T, 0>;
-    using Bwd = Stage<DK, NI, T, 1>;
     static_assert(sizeof(GradSmem<DK, NI>) <= 227 * 1024 && sizeof(PrepSmem<DK, NI>) <= 227 * 1024, "shared memory");
-    constexpr size_t chain_smem = std::max((size_t)Fwd::buffers * Fwd::size, (size_t)Bwd::buffers * Bwd::size);
-    static_assert(chain_smem <= 227 * 1024, "shared memory");
     p.slices = (p.dv + kSlice - 1) / kSlice;
-    const size_t vt = (size_t)p.slices * kC * kSlice * sizeof(T), ot = (size_t)p.slices * NI * kC * 128;
+    const size_t vt = (size_t)p.slices * kC * kSlice * sizeof(T), ot = (size_t)p.slices * NI * kC * 64;
     const size_t state = (size_t)p.dv * DK * sizeof(float), rows = (size_t)p.dv * kC * sizeof(float);
     const size_t per_head = (U::size + vt + ot + 2 * state + 2 * rows) * p.nc * p.dirs;
     const int most = (int)std::min<size_t>((size_t)p.BH, std::max<size_t>(1, kMaxWorkspace / per_head));
     const int passes = (p.BH + most - 1) / most, each_pass = (p.BH + passes - 1) / passes;
+    int dev = 0, sms = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     unsigned char *ws = nullptr;
-    cudaError_t err = ws_alloc(reinterpret_cast<void **>(&ws), per_head * each_pass, stream);
+    if (err == cudaSuccess) err = ws_alloc(reinterpret_cast<void **>(&ws), per_head * each_pass, stream);
     if (err != cudaSuccess) return err;
     for (int h = 0; h < p.BH && err == cudaSuccess; h += each_pass) {
         p.head0 = h;
         p.heads = std::min(each_pass, p.BH - h);
         const size_t n = (size_t)p.nc * p.dirs * p.heads;
+        // a chain block fills an SM's shared memory: two pairs of warps a block while those blocks fit the SMs
+        const bool wide = (long long)p.slices * p.heads * 2 * p.dirs > sms;
         p.unit = ws;
         p.vt = p.unit + n * U::size;
         p.ot = p.vt + n * vt;
@@ -1157,7 +1192,7 @@ cudaError_t run(BwdParams p, cudaStream_t stream)
         p.ZT = p.WT + n * p.dv * kC;
         err = launch(bwd_prepare_kernel<DK, NI, T>, dim3(p.nc, p.heads, p.dirs), kPrepThreads, sizeof(PrepSmem<DK, NI>), p, stream);
         if (err == cudaSuccess)
-            err = launch(bwd_chain_kernel<DK, NI, T>, dim3(p.slices, p.heads, 2 * p.dirs), kChainThreads, chain_smem, p, stream);
+            err = wide ? launch_chains<DK, NI, T, 4>(p, stream) : launch_chains<DK, NI, T, 2>(p, stream);
         if (err == cudaSuccess)
             err = launch(bwd_grad_kernel<DK, NI, T>, dim3(p.nc, p.heads), kGradThreads, sizeof(GradSmem<DK, NI>), p, stream);
     }
