@@ -190,13 +190,14 @@ __device__ __forceinline__ void frag_bt(uint32_t (&r)[4], uint32_t tile, int k, 
     ldsm_t(r, tile + sw<RB>(k + (l & 15), (n >> 3) + (l >> 4)));
 }
 
-// c (m16 x n16, two n8 tiles) += the sum of KS products A B over the terms: products of order i + j < 3 (one term
-// each: 0), the small ones first and all into a sum of their own, which an ordinary addition, rounded to nearest, adds to
-// c: the truncation of the tensor core's sums then touches every 16 KS products once and does not pile up over k.
-template <int KS, int NA, int NB>
-__device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[KS][NA][4], const uint32_t (&b)[KS][NB][4])
+// c (m16 x 16 G: 2 G tiles of n8) += the sum of KS products A B over the terms: products of order i + j < 3 (one term
+// each: 0), the small ones first and all into sums of their own, which an ordinary addition, rounded to nearest, adds to
+// c: the truncation of the tensor core's sums then touches every 16 KS products once and does not pile up over k.  The
+// 2 G sums are independent; a product waits for the one before it in its own sum only.
+template <int G, int KS, int NA, int NB>
+__device__ __forceinline__ void mma_terms(float (*c)[4], const uint32_t (&a)[KS][NA][4], const uint32_t (&b)[G][KS][NB][4])
 {
-    float d0[4] = {}, d1[4] = {};
+    float d[2 * G][4] = {};
 #pragma unroll
     for (int order = NA + NB - 2 < 2 ? NA + NB - 2 : 2; order >= 0; --order)
 #pragma unroll
@@ -205,20 +206,23 @@ __device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const 
             for (int i = 0; i < NA; ++i) {
                 const int j = order - i;
                 if (j < 0 || j >= NB) continue;
-                mma(d0, a[k][i], b[k][j][0], b[k][j][1]);
-                mma(d1, a[k][i], b[k][j][2], b[k][j][3]);
+#pragma unroll
+                for (int n = 0; n < G; ++n) {
+                    mma(d[2 * n], a[k][i], b[n][k][j][0], b[n][k][j][1]);
+                    mma(d[2 * n + 1], a[k][i], b[n][k][j][2], b[n][k][j][3]);
+                }
             }
 #pragma unroll
-    for (int x = 0; x < 4; ++x) {
-        c0[x] += d0[x];
-        c1[x] += d1[x];
-    }
+    for (int n = 0; n < 2 * G; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) c[n][x] += d[n][x];
 }
 
+// the same for one product of one n16 block
 template <int NA, int NB>
-__device__ __forceinline__ void mma_terms(float (&c0)[4], float (&c1)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4])
+__device__ __forceinline__ void mma_terms(float (*c)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4])
 {
-    mma_terms<1, NA, NB>(c0, c1, reinterpret_cast<const uint32_t (&)[1][NA][4]>(a), reinterpret_cast<const uint32_t (&)[1][NB][4]>(b));
+    mma_terms<1, 1, NA, NB>(c, reinterpret_cast<const uint32_t (&)[1][NA][4]>(a), reinterpret_cast<const uint32_t (&)[1][1][NB][4]>(b));
 }
 
 // the left operand whose columns k .. k + 15 are the accumulator tiles x, y times per-column factors
@@ -409,8 +413,8 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
             uint32_t b[NI][4];
 #pragma unroll
             for (int x = 0; x < NI; ++x) frag_b<DK * 2>(b[x], ks + x * U::kKey, k, nb);
-            mma_terms(kk[2 * n], kk[2 * n + 1], ka, b);
-            mma_terms(qk[2 * n], qk[2 * n + 1], qa, b);
+            mma_terms(kk + 2 * n, ka, b);
+            mma_terms(qk + 2 * n, qa, b);
         }
     }
 #pragma unroll
@@ -495,6 +499,30 @@ struct Stage {
     static constexpr int bytes = meet + buffers * size;
 };
 
+// c (16 x 64) += A B with B the triangular tile at tB (N or P, three terms), tokens 16 k .. of the contraction against
+// tokens n0 .. n1 - 1 (in sixteens); TRANS: B is stored [k][n]
+template <bool TRANS, int NA>
+__device__ __forceinline__ void triangle(float (*c)[4], const uint32_t (&a)[NA][4], uint32_t tB, int k, int n0, int n1)
+{
+#pragma unroll
+    for (int n = 0; n < 4; n += 2) {
+        if (n + 1 < n0 || n >= n1) continue;
+        uint32_t b[2][1][3][4];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int x = 0; x < 3; ++x) {
+                if (n + u < n0 || n + u >= n1) continue;
+                if (TRANS) frag_bt<128>(b[u][0][x], tB + x * kTri, 16 * k, 16 * (n + u));
+                else frag_b<128>(b[u][0][x], tB + x * kTri, 16 * k, 16 * (n + u));
+            }
+        const auto &a1 = reinterpret_cast<const uint32_t (&)[1][NA][4]>(a);
+        if (n >= n0 && n + 1 < n1) mma_terms<2, 1, NA, 3>(c + 2 * n, a1, b);
+        else if (n >= n0) mma_terms<1, 1, NA, 3>(c + 2 * n, a1, reinterpret_cast<const uint32_t (&)[1][1][3][4]>(b[0]));
+        else mma_terms<1, 1, NA, 3>(c + 2 * n + 2, a1, reinterpret_cast<const uint32_t (&)[1][1][3][4]>(b[1]));
+    }
+}
+
 template <int DK, int NI, typename T, int WALK, int PAIRS>
 __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char *raw)
 {
@@ -541,28 +569,28 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
             acc_to_a<3>(a[0], h[2 * k], h[2 * k + 1], one);
             acc_to_a<3>(a[1], h[2 * k + 2], h[2 * k + 3], one);
 #pragma unroll
-            for (int n = 0; n < 4; ++n) {
-                uint32_t b[2][NI][4];
+            for (int n = 0; n < 4; n += 2) {
+                uint32_t b[2][2][NI][4];
 #pragma unroll
-                for (int x = 0; x < NI; ++x) {
-                    frag_b<DK * 2>(b[0][x], tK + x * KP, k0 + 16 * k, 16 * n);
-                    frag_b<DK * 2>(b[1][x], tK + x * KP, k0 + 16 * k + 16, 16 * n);
-                }
-                mma_terms<2, 3, NI>(r[2 * n], r[2 * n + 1], a, b);
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int x = 0; x < NI; ++x)
+                        frag_b<DK * 2>(b[u >> 1][u & 1][x], tK + x * KP, k0 + 16 * (k + (u & 1)), 16 * (n + (u >> 1)));
+                mma_terms<2, 2, 3, NI>(r + 2 * n, a, b);
             }
         }
     };
     // h += A X: A the left operands of tokens 16 k .. 16 k + 31, X the tile K or Q
     auto add_outer = [&](const uint32_t (&a)[2][3][4], uint32_t tX, int k) {
 #pragma unroll
-        for (int n = 0; n < HK / 16; ++n) {
-            uint32_t b[2][NI][4];
+        for (int n = 0; n < HK / 16; n += 2) {
+            uint32_t b[2][2][NI][4];
 #pragma unroll
-            for (int x = 0; x < NI; ++x) {
-                frag_bt<DK * 2>(b[0][x], tX + x * KP, 16 * k, k0 + 16 * n);
-                frag_bt<DK * 2>(b[1][x], tX + x * KP, 16 * k + 16, k0 + 16 * n);
-            }
-            mma_terms<2, 3, NI>(h[2 * n], h[2 * n + 1], a, b);
+            for (int u = 0; u < 4; ++u)
+#pragma unroll
+                for (int x = 0; x < NI; ++x)
+                    frag_bt<DK * 2>(b[u >> 1][u & 1][x], tX + x * KP, 16 * (k + (u & 1)), k0 + 16 * (n + (u >> 1)));
+            mma_terms<2, 2, 3, NI>(h + 2 * n, a, b);
         }
     };
     // adds the other warp's part of r to this one's
@@ -636,13 +664,7 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
                 uint32_t a[3][4];
                 factors(f, k, [&](int i) { return -gt.b[i]; });
                 acc_to_a<3>(a, r[2 * k], r[2 * k + 1], f);
-#pragma unroll
-                for (int n = k; n < 4; ++n) {
-                    uint32_t b[3][4];
-#pragma unroll
-                    for (int x = 0; x < 3; ++x) frag_b<128>(b[x], tN + x * kTri, 16 * k, 16 * n);
-                    mma_terms(w[2 * n], w[2 * n + 1], a, b);
-                }
+                triangle<false>(w, a, tN, k, k, 4);
             }
         } else {
             const uint32_t tQ = base + so + (uint32_t)U::Q, tP = base + so + (uint32_t)U::P;
@@ -662,13 +684,7 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
 #pragma unroll
                     for (int x = 0; x < NI; ++x) frag_at<64>(o[x], tX + x * (kC * 64), 16 * (pair & 1), 16 * kk);
                     if ((kk == 0 || kk == 3) == (half == 0)) {
-#pragma unroll
-                        for (int n = 0; n <= kk; ++n) {
-                            uint32_t b[3][4];
-#pragma unroll
-                            for (int x = 0; x < 3; ++x) frag_bt<128>(b[x], tP + x * kTri, 16 * kk, 16 * n);
-                            mma_terms(r[2 * n], r[2 * n + 1], o, b);
-                        }
+                        triangle<true>(r, o, tP, kk, 0, kk + 1);
                     }
                     float f[4], u[4] = {}, v[4] = {};
                     factors(f, kk, [&](int i) { return gt.gam[i]; });
@@ -693,13 +709,7 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
                 uint32_t a[3][4];
                 factors(f, k, [&](int i) { return -gt.b[i]; });
                 acc_to_a<3>(a, r[2 * k], r[2 * k + 1], f);
-#pragma unroll
-                for (int n = 0; n <= k; ++n) {
-                    uint32_t b[3][4];
-#pragma unroll
-                    for (int x = 0; x < 3; ++x) frag_bt<128>(b[x], tN + x * kTri, 16 * k, 16 * n);
-                    mma_terms(w[2 * n], w[2 * n + 1], a, b);
-                }
+                triangle<true>(w, a, tN, k, 0, k + 1);
             }
         }
         float *out = (WALK ? p.ZT : p.WT) + (ws * p.dv + row) * kC;
@@ -922,11 +932,11 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
                     uint32_t b[3][4];
 #pragma unroll
                     for (int x = 0; x < 3; ++x) frag_bt<DK * 2>(b[x], aH + x * Sm::kState, k, wn * (DK / 2) + 16 * n);
-                    mma_terms(hdo[2 * n], hdo[2 * n + 1], o, b);
-                    mma_terms(hy[2 * n], hy[2 * n + 1], y, b);
+                    mma_terms(hdo + 2 * n, o, b);
+                    mma_terms(hy + 2 * n, y, b);
 #pragma unroll
                     for (int x = 0; x < 3; ++x) frag_bt<DK * 2>(b[x], aG + x * Sm::kState, k, wn * (DK / 2) + 16 * n);
-                    mma_terms(du[2 * n], du[2 * n + 1], u, b);
+                    mma_terms(du + 2 * n, u, b);
                 }
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
@@ -934,8 +944,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
                     uint32_t b[3][4];
 #pragma unroll
                     for (int x = 0; x < 3; ++x) frag_bt<128>(b[x], aU + x * Sm::kVal, k, 32 * wn + 16 * n);
-                    mma_terms(dp[2 * n], dp[2 * n + 1], o, b);
-                    mma_terms(dx[2 * n], dx[2 * n + 1], y, b);
+                    mma_terms(dp + 2 * n, o, b);
+                    mma_terms(dx + 2 * n, y, b);
                 }
             }
             if (!Sm::kStage && c0 + kStep < p.dv) {
@@ -970,8 +980,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
                 uint32_t b[NI][4];
 #pragma unroll
                 for (int x = 0; x < NI; ++x) frag_b<DK * 2>(b[x], aK + x * (int)U::kKey, k, nb);
-                mma_terms(kk[2 * n], kk[2 * n + 1], ka, b);
-                mma_terms(qk[2 * n], qk[2 * n + 1], qa, b);
+                mma_terms(kk + 2 * n, ka, b);
+                mma_terms(qk + 2 * n, qa, b);
             }
         }
         __syncthreads();               // the walk's planes are done with: E, F, M take their place
@@ -1085,17 +1095,17 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
                 if (k <= wm) {
 #pragma unroll
                     for (int x = 0; x < NE; ++x) frag_a<128>(a[x], aE + x * kTri, 16 * wm, 16 * k);
-                    mma_terms(hdo[2 * n], hdo[2 * n + 1], a, b);
+                    mma_terms(hdo + 2 * n, a, b);
                 }
 #pragma unroll
                 for (int x = 0; x < NE; ++x) frag_a<128>(a[x], aS + x * kTri, 16 * wm, 16 * k);
-                mma_terms(hy[2 * n], hy[2 * n + 1], a, b);
+                mma_terms(hy + 2 * n, a, b);
                 if (k >= wm) {
 #pragma unroll
                     for (int x = 0; x < NI; ++x) frag_bt<DK * 2>(b[x], aQ + x * (int)U::kKey, 16 * k, nb);
 #pragma unroll
                     for (int x = 0; x < NE; ++x) frag_at<128>(a[x], aE + x * kTri, 16 * wm, 16 * k);
-                    mma_terms(hy[2 * n], hy[2 * n + 1], a, b);
+                    mma_terms(hy + 2 * n, a, b);
                 }
             }
         }

@@ -307,12 +307,16 @@ cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t stream)
     }
     p.positions = a.positions;
     p.pos_sb = a.pos_sb;
-    for (int q = 0, axis = 0, i = 0; q < a.d / 2; ++q, ++i) {
-        while (2 * i >= a.axes[axis]) {
-            ++axis;
-            i = 0;
+    double *f = p.freq;
+    for (int n : a.axes) {
+        // theta^(-2 i / n) for i = 8 u + v as a product of two powers: a quarter of the calls of pow, which would
+        // otherwise be most of the host's time
+        double low[8];
+        for (int v = 0; v < 8 && 2 * v < n; ++v) low[v] = std::pow(a.theta, -2.0 * v / n);
+        for (int i = 0; 2 * i < n; i += 8) {
+            const double high = std::pow(a.theta, -2.0 * i / n) / 6.283185307179586476925;
+            for (int v = 0; v < 8 && 2 * (i + v) < n; ++v) *f++ = high * low[v];
         }
-        p.freq[q] = std::pow(a.theta, -2.0 * i / a.axes[axis]) / 6.283185307179586476925;
     }
     p.end_t = a.axes[0] / 2;
     p.end_h = p.end_t + a.axes[1] / 2;

@@ -5,7 +5,6 @@ and passes raw pointers and sizes to the library; all computation happens in
 the library's CUDA kernels.  There is no CPU or fallback path: if libgdn.so
 cannot be loaded, calls raise.
 """
-import contextlib
 import ctypes
 import os
 
@@ -178,15 +177,13 @@ def gdn_forward(q, k, v, beta, decay, state_in=None, *, bidi=False, recurrent=Fa
     return o, state_out
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """Runs a call with its tensors' device current, and its outputs allocated on the stream that writes them."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield torch.cuda.current_stream(device).cuda_stream
-        else:
-            with torch.cuda.stream(stream):
-                yield stream.cuda_stream
+def _run(device, stream, call):
+    """call(handle) with the tensors' device current, and outputs allocated on the stream that writes them; handle is
+    that stream's.  The usual case, the current device and its current stream, switches nothing."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
+    with torch.cuda.device(device), torch.cuda.stream(stream):
+        return call(torch._C._cuda_getCurrentRawStream(device.index))
 
 
 def gdn_backward(q, k, v, beta, decay, do, state_in=None, dstate=None, *, bidi=False, stream=None):
@@ -217,14 +214,17 @@ def gdn_backward(q, k, v, beta, decay, do, state_in=None, dstate=None, *, bidi=F
     if dstate is not None:
         _expect(dstate, "dstate", ((2,) if bidi else ()) + (B, H, dk, dv), torch.float32, dev)
     lib = load_library()
-    with _on(dev, stream) as handle:
+
+    def call(handle):
         dq, dk_, dv_ = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
         db, da = torch.empty_like(beta), torch.empty_like(decay)
-        ds = torch.empty(B, H, dk, dv, dtype=torch.float32, device=dev)
+        ds = q.new_empty((B, H, dk, dv), dtype=torch.float32)
         _check(lib.gdn_backward(_ptr(q), _ptr(k), _ptr(v), _ptr(beta), _ptr(decay), _ptr(state_in), _ptr(do),
                                 _ptr(dstate), _ptr(dq), _ptr(dk_), _ptr(dv_), _ptr(db), _ptr(da), _ptr(ds),
                                 B, H, T, dk, dv, mode, handle))
-    return dq, dk_, dv_, db, da, ds
+        return dq, dk_, dv_, db, da, ds
+
+    return _run(dev, stream, call)
 
 
 def gdn_forward_segmented(q, k, v, beta, decay, state_in=None, *, n_segments=4, o=None,

@@ -9,7 +9,7 @@ from typing import NamedTuple, Optional
 
 import torch
 
-from .gdn import GDN_FP32, View, _check, _on, _ptr, gdn_backward, gdn_forward, load_library
+from .gdn import GDN_FP32, View, _check, _ptr, _run, gdn_backward, gdn_forward, load_library
 
 GDN_ROTARY_HALF = 16
 GDN_ROTARY_L2 = 32
@@ -19,7 +19,7 @@ _DTYPES = {torch.bfloat16: 0, torch.float32: GDN_FP32}
 
 def _rows(t, name, shape, dtype, device):
     """A [B,H,T,d] tensor of any strides with contiguous rows, as a gdn_view."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
@@ -38,13 +38,21 @@ def _shape(t, name):
         raise ValueError("runs on CUDA tensors only")
     if t.dtype not in _DTYPES:
         raise TypeError(f"{name} must be bf16 or fp32, got {t.dtype}")
-    return tuple(t.shape)
+    return t.shape
 
 
-def _tokens_first(shape, like):
-    """An empty logical [B,H,T,d] tensor in [B,T,H,d] memory."""
+def _heads_first(like, shape):
+    """An empty [B,H,T,d] tensor, and its gdn_view."""
     B, H, T, d = shape
-    return torch.empty((B, T, H, d), dtype=like.dtype, device=like.device).transpose(1, 2)
+    t = like.new_empty(shape)
+    return t, View(t.data_ptr(), H * T * d, T * d, d)
+
+
+def _tokens_first(like, shape):
+    """An empty [B,T,H,d] tensor, and the gdn_view of its [B,H,T,d] transpose."""
+    B, H, T, d = shape
+    t = like.new_empty((B, T, H, d))
+    return t, View(t.data_ptr(), T * H * d, d, H * d)
 
 
 def _turns(axes, grid, start, positions, theta, eps, shape, device):
@@ -88,12 +96,14 @@ def gdn_rotary(q, k=None, *, axes, grid=None, start=0, positions=None, theta=100
     mode = _DTYPES[q.dtype] | (GDN_ROTARY_HALF if half else 0) | (GDN_ROTARY_L2 if l2norm else 0)
     vq = _rows(q, "q", shape, q.dtype, dev)
     vk = None if k is None else _rows(k, "k", shape, q.dtype, dev)
-    with _on(dev, stream) as handle:
-        yq = torch.empty(shape, dtype=q.dtype, device=dev)
-        yk = None if k is None else torch.empty(shape, dtype=q.dtype, device=dev)
-        _check(lib.gdn_rotary(vq, vk, _rows(yq, "q", shape, q.dtype, dev),
-                              None if k is None else _rows(yk, "k", shape, q.dtype, dev), *how, mode, handle))
-    return yq if k is None else (yq, yk)
+
+    def call(handle):
+        yq, to_q = _heads_first(q, shape)
+        yk, to_k = (None, None) if k is None else _heads_first(q, shape)
+        _check(lib.gdn_rotary(vq, vk, to_q, to_k, *how, mode, handle))
+        return yq if k is None else (yq, yk)
+
+    return _run(dev, stream, call)
 
 
 def gdn_rotary_backward(dq, dk=None, q=None, k=None, *, axes, grid=None, start=0, positions=None, theta=10000.0,
@@ -117,12 +127,14 @@ def gdn_rotary_backward(dq, dk=None, q=None, k=None, *, axes, grid=None, start=0
         vx[0] = _rows(q, "q", shape, dq.dtype, dev)
         if dk is not None:
             vx[1] = _rows(k, "k", shape, dq.dtype, dev)
-    with _on(dev, stream) as handle:
-        yq = _tokens_first(shape, dq)
-        yk = None if dk is None else _tokens_first(shape, dq)
-        _check(lib.gdn_rotary_backward(*vg, *vx, _rows(yq, "q", shape, dq.dtype, dev),
-                                       None if dk is None else _rows(yk, "k", shape, dq.dtype, dev), *how, mode, handle))
-    return yq if dk is None else (yq, yk)
+
+    def call(handle):
+        yq, to_q = _tokens_first(dq, shape)
+        yk, to_k = (None, None) if dk is None else _tokens_first(dq, shape)
+        _check(lib.gdn_rotary_backward(*vg, *vx, to_q, to_k, *how, mode, handle))
+        return yq.transpose(1, 2) if dk is None else (yq.transpose(1, 2), yk.transpose(1, 2))
+
+    return _run(dev, stream, call)
 
 
 def _weight(weight, H, dv, device):
@@ -130,7 +142,7 @@ def _weight(weight, H, dv, device):
         return 0
     if weight.dtype != torch.float32:
         raise TypeError(f"weight: expected torch.float32, got {weight.dtype}")
-    if tuple(weight.shape) not in ((dv,), (H, dv)):
+    if weight.shape not in ((dv,), (H, dv)):
         raise ValueError(f"weight: expected shape ({dv},) or ({H}, {dv}), got {tuple(weight.shape)}")
     if weight.device != device:
         raise ValueError(f"weight: expected device {device}, got {weight.device}")
@@ -152,11 +164,14 @@ def gdn_gated_norm(o, gate=None, weight=None, *, eps=1e-5, stream=None):
     per_head = _weight(weight, H, dv, dev)
     vo = _rows(o, "o", shape, o.dtype, dev)
     vg = None if gate is None else _rows(gate, "gate", shape, o.dtype, dev)
-    with _on(dev, stream) as handle:
-        y = _tokens_first(shape, o)
-        _check(lib.gdn_gated_norm(vo, vg, _ptr(weight), per_head, _rows(y, "y", shape, o.dtype, dev), B, H, T, dv, eps,
-                                  _DTYPES[o.dtype], handle))
-    return y.transpose(1, 2).view(B, T, H * dv)
+
+    def call(handle):
+        y = o.new_empty((B, T, H * dv))
+        _check(lib.gdn_gated_norm(vo, vg, _ptr(weight), per_head, View(y.data_ptr(), T * H * dv, dv, H * dv), B, H, T, dv,
+                                  eps, _DTYPES[o.dtype], handle))
+        return y
+
+    return _run(dev, stream, call)
 
 
 def gdn_gated_norm_backward(dy, o, gate=None, weight=None, *, eps=1e-5, stream=None):
@@ -166,21 +181,28 @@ def gdn_gated_norm_backward(dy, o, gate=None, weight=None, *, eps=1e-5, stream=N
     B, H, T, dv = shape
     dev, lib = o.device, load_library()
     per_head = _weight(weight, H, dv, dev)
-    if tuple(dy.shape) != (B, T, H * dv):
+    if dy.shape != (B, T, H * dv):
         raise ValueError(f"dy: expected shape {(B, T, H * dv)}, got {tuple(dy.shape)}")
-    if dy.stride(2) != 1 and H * dv != 1:
+    if dy.dtype != o.dtype:
+        raise TypeError(f"dy: expected {o.dtype}, got {dy.dtype}")
+    if dy.device != dev:
+        raise ValueError(f"dy: expected device {dev}, got {dy.device}")
+    sb, st, sd = dy.stride()
+    if sd != 1 and H * dv != 1:
         raise ValueError("dy: rows (the last dimension) must be contiguous")
-    vdy = _rows(dy.unflatten(2, (H, dv)).transpose(1, 2), "dy", shape, o.dtype, dev)
+    vdy = View(dy.data_ptr(), sb, dv, st)
     vo = _rows(o, "o", shape, o.dtype, dev)
     vg = None if gate is None else _rows(gate, "gate", shape, o.dtype, dev)
-    with _on(dev, stream) as handle:
-        do = torch.empty(shape, dtype=o.dtype, device=dev)
-        dgate = None if gate is None else _tokens_first(shape, o)
+
+    def call(handle):
+        do, to_o = _heads_first(o, shape)
+        dgate, to_g = (None, None) if gate is None else _tokens_first(o, shape)
         dw = None if weight is None else torch.empty_like(weight)
-        _check(lib.gdn_gated_norm_backward(vdy, vo, vg, _ptr(weight), per_head, _rows(do, "do", shape, o.dtype, dev),
-                                           None if gate is None else _rows(dgate, "dgate", shape, o.dtype, dev),
-                                           _ptr(dw), B, H, T, dv, eps, _DTYPES[o.dtype], handle))
-    return do, dgate, dw
+        _check(lib.gdn_gated_norm_backward(vdy, vo, vg, _ptr(weight), per_head, to_o, to_g, _ptr(dw), B, H, T, dv, eps,
+                                           _DTYPES[o.dtype], handle))
+        return do, None if gate is None else dgate.transpose(1, 2), dw
+
+    return _run(dev, stream, call)
 
 
 class LayerSaved(NamedTuple):
@@ -213,8 +235,7 @@ def gdn_layer_forward(q, k, v, beta, decay, gate=None, weight=None, state_in=Non
     """
     how = dict(axes=axes, grid=grid, start=start, positions=positions, theta=theta, half=half, l2norm=l2norm, eps=eps)
     qr, kr = gdn_rotary(q, k, **how, stream=stream)
-    with _on(q.device, stream):
-        o, state = gdn_forward(qr, kr, v, beta, decay, state_in, bidi=bidi, stream=stream)
+    o, state = _run(q.device, stream, lambda _: gdn_forward(qr, kr, v, beta, decay, state_in, bidi=bidi, stream=stream))
     y = gdn_gated_norm(o, gate, weight, eps=norm_eps, stream=stream)
     return y, state, LayerSaved(q, k, qr, kr, v, beta, decay, state_in, o, gate, weight, bidi, norm_eps, how)
 
