@@ -38,231 +38,15 @@
 //   operands of the next product; so the walk's three dependent products pass through registers, no state goes through
 //   shared memory, and the block's barrier only paces the double-buffered operands.
 // * gradients (a block per chunk, both scan directions, so that a bidirectional call's sums are rounded once).
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
-
 #include <algorithm>
 #include <cstdint>
 
-#include "gdn_internal.h"
-#include "sm100_ptx.cuh"
+#include "gdn_backward.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kC = 64;             // tokens per chunk
-constexpr int kSlice = 32;         // dv columns of a V or dO tile
-constexpr int kTri = kC * kC * 2;  // bytes of one term plane of N or P
-
-__device__ __forceinline__ float ldf(const float *p) { return *p; }
-__device__ __forceinline__ float ldf(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void st2(float *p, float x, float y) { *reinterpret_cast<float2 *>(p) = make_float2(x, y); }
-__device__ __forceinline__ void st2(__nv_bfloat16 *p, float x, float y)
-{
-    *reinterpret_cast<__nv_bfloat162 *>(p) = __floats2bfloat162_rn(x, y);
-}
-
-// Gates of a chunk in scan order, as prepare leaves them for the other kernels.  a is clamped as in the
-// forward kernels; behind the sequence's end a = 1 and b = 0.  The running sums of log2 a are held in 64 bits: a strong
-// decay brings them to several hundred within a chunk, where 32 bits would leave differences of neighbours 1e-5 off.
-struct Gates {
-    float gam[kC], e[kC], b[kC], a[kC];
-    double G[kC];
-};
-
-// Workspace of one (direction, head, chunk), in bytes.  Tiles are row-major with the 16-byte pieces of a
-// row XOR-ed by the row's number, so that eight rows' pieces of one column lie in eight bank groups.
-template <int DK, int NI>
-struct Unit {
-    static constexpr size_t kKey = (size_t)kC * DK * 2;    // one term plane of K or Q
-    static constexpr size_t gates = 0;
-    static constexpr size_t N = sizeof(Gates);             // three planes [i][j]
-    static constexpr size_t K = N + 3 * kTri;              // NI planes [token][dk]
-    static constexpr size_t Q = K + NI * kKey;
-    static constexpr size_t P = Q + NI * kKey;             // three planes [i][j]
-    static constexpr size_t size = P + 3 * kTri;
-    static_assert(N % 128 == 0 && size % 128 == 0, "tiles start on 128-byte boundaries");
-};
-
-struct BwdParams {
-    const void *q, *k, *v, *dout;
-    const float *beta, *decay, *state_in, *dstate;
-    void *dq, *dk_, *dv_;
-    float *dbeta, *ddecay, *dstate_in;
-    // workspace of this launch's heads, one entry per (direction, head, chunk)
-    unsigned char *unit;       // Unit<DK, NI>
-    unsigned char *vt;         // [slice][64 tokens][32 columns] of the input type
-    unsigned char *ot;         // [slice][NI planes][64 tokens][32 columns]
-    float *HT, *GT;            // [dv][DK]: H0 and dH1, transposed
-    float *WT, *ZT;            // [dv][64 tokens]
-    int head0, heads;          // the heads [head0, head0 + heads) of B*H
-    int BH, T, nc, dk, dv, dirs, slices;
-};
-
-// A chunk of one scan: its tokens in scan order.  Chunks are tiles [64 c, 64 c + n) of the sequence for
-// both directions; the reverse scan walks tiles and tokens downwards.
-struct Tile {
-    int dir, head, c, n;       // head: index in B*H
-    size_t ws;                 // index of the (direction, head, chunk) entry in the workspace
-    __device__ __forceinline__ int tok(int i) const { return c * kC + (dir ? n - 1 - i : i); }
-};
-
-__device__ __forceinline__ Tile make_tile(const BwdParams &p, int dir, int local_head, int c)
-{
-    Tile t;
-    t.dir = dir;
-    t.head = p.head0 + local_head;
-    t.c = c;
-    t.n = min(kC, p.T - c * kC);
-    t.ws = ((size_t)dir * p.heads + local_head) * p.nc + c;
-    return t;
-}
-
-// ---------------------------------------------------------------- terms, fragments, products
-// two values as packed bf16 pairs (x in the low half): terms of x and y
-template <int NT>
-__device__ __forceinline__ void split2(float x, float y, uint32_t (&out)[NT])
-{
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
-        out[t] = *reinterpret_cast<const uint32_t *>(&v);
-        if (t + 1 < NT) {
-            x -= __uint_as_float(out[t] << 16);
-            y -= __uint_as_float(out[t] & 0xffff0000u);
-        }
-    }
-}
-
-__device__ __forceinline__ float lo16(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float hi16(uint32_t u) { return __uint_as_float(u & 0xffff0000u); }
-
-// byte offset of the 16-byte piece `piece` of row `row` in a swizzled tile with RB-byte rows
-template <int RB>
-__device__ __forceinline__ uint32_t sw(int row, int piece)
-{
-    return row * RB + ((piece ^ (RB == 64 ? (row >> 1) & 3 : row & 7)) << 4);
-}
-
-__device__ __forceinline__ void ldsm(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm_t(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
-}
-// c += A B.  The tensor core's fp32 sums are truncated, not rounded.
-__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1)
-{
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-        "{%0, %1, %2, %3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// Fragments of a 16 x 16 block of a tile at shared address `tile`.  A from [m][k] storage, A from [k][m] storage; B
-// (two n8 halves: r[0], r[1] and r[2], r[3]) from [n][k] storage, B from [k][n] storage.
-template <int RB>
-__device__ __forceinline__ void frag_a(uint32_t (&r)[4], uint32_t tile, int m, int k)
-{
-    const int l = threadIdx.x & 31;
-    ldsm(r, tile + sw<RB>(m + (l & 15), (k >> 3) + (l >> 4)));
-}
-template <int RB>
-__device__ __forceinline__ void frag_at(uint32_t (&r)[4], uint32_t tile, int m, int k)
-{
-    const int l = threadIdx.x & 31;
-    ldsm_t(r, tile + sw<RB>(k + (l & 7) + ((l >> 4) << 3), (m >> 3) + ((l >> 3) & 1)));
-}
-template <int RB>
-__device__ __forceinline__ void frag_b(uint32_t (&r)[4], uint32_t tile, int k, int n)
-{
-    const int l = threadIdx.x & 31;
-    ldsm(r, tile + sw<RB>(n + (l & 7) + ((l >> 4) << 3), (k >> 3) + ((l >> 3) & 1)));
-}
-template <int RB>
-__device__ __forceinline__ void frag_bt(uint32_t (&r)[4], uint32_t tile, int k, int n)
-{
-    const int l = threadIdx.x & 31;
-    ldsm_t(r, tile + sw<RB>(k + (l & 15), (n >> 3) + (l >> 4)));
-}
-
-// c (m16 x 16 G: 2 G tiles of n8) += the sum of KS products A B over the terms: products of order i + j < 3 (one term
-// each: 0), the small ones first and all into sums of their own, which an ordinary addition, rounded to nearest, adds to
-// c: the truncation of the tensor core's sums then touches every 16 KS products once and does not pile up over k.  The
-// 2 G sums are independent; a product waits for the one before it in its own sum only.
-template <int G, int KS, int NA, int NB>
-__device__ __forceinline__ void mma_terms(float (*c)[4], const uint32_t (&a)[KS][NA][4], const uint32_t (&b)[G][KS][NB][4])
-{
-    float d[2 * G][4] = {};
-#pragma unroll
-    for (int order = NA + NB - 2 < 2 ? NA + NB - 2 : 2; order >= 0; --order)
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int i = 0; i < NA; ++i) {
-                const int j = order - i;
-                if (j < 0 || j >= NB) continue;
-#pragma unroll
-                for (int n = 0; n < G; ++n) {
-                    mma(d[2 * n], a[k][i], b[n][k][j][0], b[n][k][j][1]);
-                    mma(d[2 * n + 1], a[k][i], b[n][k][j][2], b[n][k][j][3]);
-                }
-            }
-#pragma unroll
-    for (int n = 0; n < 2 * G; ++n)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) c[n][x] += d[n][x];
-}
-
-// the same for one product of one n16 block
-template <int NA, int NB>
-__device__ __forceinline__ void mma_terms(float (*c)[4], const uint32_t (&a)[NA][4], const uint32_t (&b)[NB][4])
-{
-    mma_terms<1, 1, NA, NB>(c, reinterpret_cast<const uint32_t (&)[1][NA][4]>(a), reinterpret_cast<const uint32_t (&)[1][1][NB][4]>(b));
-}
-
-// the left operand whose columns k .. k + 15 are the accumulator tiles x, y times per-column factors
-// f[0..1] (columns 2 t, 2 t + 1 of x) and f[2..3] (of y)
-template <int NT>
-__device__ __forceinline__ void acc_to_a(uint32_t (&a)[NT][4], const float (&x)[4], const float (&y)[4], const float (&f)[4])
-{
-    uint32_t u[NT];
-    split2<NT>(x[0] * f[0], x[1] * f[1], u);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) a[t][0] = u[t];
-    split2<NT>(x[2] * f[0], x[3] * f[1], u);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) a[t][1] = u[t];
-    split2<NT>(y[0] * f[2], y[1] * f[3], u);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) a[t][2] = u[t];
-    split2<NT>(y[2] * f[2], y[3] * f[3], u);
-#pragma unroll
-    for (int t = 0; t < NT; ++t) a[t][3] = u[t];
-}
-
-__device__ __forceinline__ void copy16(uint32_t dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
-
-__device__ __forceinline__ void copy_block(uint32_t dst, const unsigned char *src, int bytes)
-{
-    for (int o = threadIdx.x * 16; o < bytes; o += blockDim.x * 16) copy16(dst + o, src + o);
-}
-
-__device__ __forceinline__ float warp_sum(float x)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    return x;
-}
+using namespace bwd;
 
 // ---------------------------------------------------------------- prepare
 // Grid (chunks, heads, directions), 256 threads.
@@ -368,9 +152,9 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
         const size_t row = on ? (size_t)t.tok(i) * p.dk : 0;
         float x[8];
         get8(kb + row, on, 8 * c, p.dk, x);
-        put8<NI, DK * 2, T>(x, i, c, s.K, unit + U::K, U::kKey);
+        put8<NI, kKeyRow<DK>, T>(x, i, c, s.K, unit + U::K, U::kKey);
         get8(qb + row, on, 8 * c, p.dk, x);
-        put8<NI, DK * 2, T>(x, i, c, s.Q, unit + U::Q, U::kKey);
+        put8<NI, kKeyRow<DK>, T>(x, i, c, s.Q, unit + U::Q, U::kKey);
     }
     const T *vb = static_cast<const T *>(p.v) + (size_t)t.head * p.T * p.dv;
     const T *ob = static_cast<const T *>(p.dout) + (size_t)t.head * p.T * p.dv;
@@ -403,8 +187,8 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
         uint32_t ka[NI][4], qa[NI][4];
 #pragma unroll
         for (int x = 0; x < NI; ++x) {
-            frag_a<DK * 2>(ka[x], ks + x * U::kKey, 16 * wm, k);
-            frag_a<DK * 2>(qa[x], qs + x * U::kKey, 16 * wm, k);
+            frag_a<kKeyRow<DK>>(ka[x], ks + x * U::kKey, 16 * wm, k);
+            frag_a<kKeyRow<DK>>(qa[x], qs + x * U::kKey, 16 * wm, k);
         }
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
@@ -412,7 +196,7 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
             if (nb > 16 * wm) continue;
             uint32_t b[NI][4];
 #pragma unroll
-            for (int x = 0; x < NI; ++x) frag_b<DK * 2>(b[x], ks + x * U::kKey, k, nb);
+            for (int x = 0; x < NI; ++x) frag_b<kKeyRow<DK>>(b[x], ks + x * U::kKey, k, nb);
             mma_terms(kk + 2 * n, ka, b);
             mma_terms(qk + 2 * n, qa, b);
         }
@@ -575,7 +359,7 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
                 for (int u = 0; u < 4; ++u)
 #pragma unroll
                     for (int x = 0; x < NI; ++x)
-                        frag_b<DK * 2>(b[u >> 1][u & 1][x], tK + x * KP, k0 + 16 * (k + (u & 1)), 16 * (n + (u >> 1)));
+                        frag_b<kKeyRow<DK>>(b[u >> 1][u & 1][x], tK + x * KP, k0 + 16 * (k + (u & 1)), 16 * (n + (u >> 1)));
                 mma_terms<2, 2, 3, NI>(r + 2 * n, a, b);
             }
         }
@@ -589,7 +373,7 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
             for (int u = 0; u < 4; ++u)
 #pragma unroll
                 for (int x = 0; x < NI; ++x)
-                    frag_bt<DK * 2>(b[u >> 1][u & 1][x], tX + x * KP, 16 * (k + (u & 1)), k0 + 16 * (n + (u >> 1)));
+                    frag_bt<kKeyRow<DK>>(b[u >> 1][u & 1][x], tX + x * KP, 16 * (k + (u & 1)), k0 + 16 * (n + (u >> 1)));
             mma_terms<2, 2, 3, NI>(h + 2 * n, a, b);
         }
     };
@@ -795,30 +579,6 @@ __device__ __forceinline__ void copy_rows(float *dst, int ld, const float *src, 
         copy16(ptx::smem_u32(dst + (e / per) * ld + 4 * (e % per)), src + (size_t)(e / per) * len + 4 * (e % per));
 }
 
-// 8 floats to term planes in a swizzled tile
-template <int RB>
-__device__ __forceinline__ void planes8(const float (&x)[8], int row, int piece, unsigned char *to, int plane)
-{
-    uint32_t w[3][4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t u[3];
-        split2<3>(x[2 * i], x[2 * i + 1], u);
-#pragma unroll
-        for (int t = 0; t < 3; ++t) w[t][i] = u[t];
-    }
-#pragma unroll
-    for (int t = 0; t < 3; ++t)
-        *reinterpret_cast<uint4 *>(to + t * plane + sw<RB>(row, piece)) = make_uint4(w[t][0], w[t][1], w[t][2], w[t][3]);
-}
-
-__device__ __forceinline__ void get8f(const float *p, float (&x)[8])
-{
-    const float4 u = reinterpret_cast<const float4 *>(p)[0], v = reinterpret_cast<const float4 *>(p)[1];
-    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-    x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-}
-
 // columns j, j + 1 of row i of a tile of term planes
 template <int NI, int RB>
 __device__ __forceinline__ float2 pair_at(const unsigned char *tile, int plane, int i, int j)
@@ -970,8 +730,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
             uint32_t ka[NI][4], qa[NI][4];
 #pragma unroll
             for (int x = 0; x < NI; ++x) {
-                frag_a<DK * 2>(ka[x], aK + x * (int)U::kKey, 16 * wm, k);
-                frag_a<DK * 2>(qa[x], aQ + x * (int)U::kKey, 16 * wm, k);
+                frag_a<kKeyRow<DK>>(ka[x], aK + x * (int)U::kKey, 16 * wm, k);
+                frag_a<kKeyRow<DK>>(qa[x], aQ + x * (int)U::kKey, 16 * wm, k);
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
@@ -979,7 +739,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
                 if (nb > 16 * wm) continue;
                 uint32_t b[NI][4];
 #pragma unroll
-                for (int x = 0; x < NI; ++x) frag_b<DK * 2>(b[x], aK + x * (int)U::kKey, k, nb);
+                for (int x = 0; x < NI; ++x) frag_b<kKeyRow<DK>>(b[x], aK + x * (int)U::kKey, k, nb);
                 mma_terms(kk + 2 * n, ka, b);
                 mma_terms(qk + 2 * n, qa, b);
             }
@@ -1014,7 +774,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const int j = wn * (DK / 2) + 8 * n + q2;
-                const float2 k = pair_at<NI, DK * 2>(s.K, (int)U::kKey, i, j), q = pair_at<NI, DK * 2>(s.Q, (int)U::kKey, i, j);
+                const float2 k = pair_at<NI, kKeyRow<DK>>(s.K, (int)U::kKey, i, j), q = pair_at<NI, kKeyRow<DK>>(s.Q, (int)U::kKey, i, j);
                 float *a = &hdo[n][2 * h], *b = &hy[n][2 * h], *c = &du[n][2 * h];
                 x = fmaf(q.x, a[0], fmaf(q.y, a[1], fmaf(-k.x, b[0], fmaf(-k.y, b[1], x))));
                 y = fmaf(k.x, c[0], fmaf(k.y, c[1], y));
@@ -1091,7 +851,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
             for (int n = 0; n < NT / 2; ++n) {
                 const int nb = wn * (DK / 2) + 16 * n;
 #pragma unroll
-                for (int x = 0; x < NI; ++x) frag_bt<DK * 2>(b[x], aK + x * (int)U::kKey, 16 * k, nb);
+                for (int x = 0; x < NI; ++x) frag_bt<kKeyRow<DK>>(b[x], aK + x * (int)U::kKey, 16 * k, nb);
                 if (k <= wm) {
 #pragma unroll
                     for (int x = 0; x < NE; ++x) frag_a<128>(a[x], aE + x * kTri, 16 * wm, 16 * k);
@@ -1102,7 +862,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
                 mma_terms(hy + 2 * n, a, b);
                 if (k >= wm) {
 #pragma unroll
-                    for (int x = 0; x < NI; ++x) frag_bt<DK * 2>(b[x], aQ + x * (int)U::kKey, 16 * k, nb);
+                    for (int x = 0; x < NI; ++x) frag_bt<kKeyRow<DK>>(b[x], aQ + x * (int)U::kKey, 16 * k, nb);
 #pragma unroll
                     for (int x = 0; x < NE; ++x) frag_at<128>(a[x], aE + x * kTri, 16 * wm, 16 * k);
                     mma_terms(hy + 2 * n, a, b);
@@ -1203,8 +963,10 @@ cudaError_t run(BwdParams p, cudaStream_t stream)
         err = launch(bwd_prepare_kernel<DK, NI, T>, dim3(p.nc, p.heads, p.dirs), kPrepThreads, sizeof(PrepSmem<DK, NI>), p, stream);
         if (err == cudaSuccess)
             err = wide ? launch_chains<DK, NI, T, 4>(p, stream) : launch_chains<DK, NI, T, 2>(p, stream);
-        if (err == cudaSuccess)
-            err = launch(bwd_grad_kernel<DK, NI, T>, dim3(p.nc, p.heads), kGradThreads, sizeof(GradSmem<DK, NI>), p, stream);
+        if (err == cudaSuccess) {
+            if constexpr (DK == 128 && NI == 1) err = launch_grad_tc(p, stream);
+            else err = launch(bwd_grad_kernel<DK, NI, T>, dim3(p.nc, p.heads), kGradThreads, sizeof(GradSmem<DK, NI>), p, stream);
+        }
     }
     const cudaError_t e2 = ws_free(ws, stream);
     return err != cudaSuccess ? err : e2;
