@@ -137,8 +137,10 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
             if (lane >= o) sum += y;
         }
         const double end = __shfl_sync(0xffffffffu, sum, 31), first = sum - l[1];
-        s.g.G[2 * lane] = first;
-        s.g.G[2 * lane + 1] = sum;
+        s.g.high[2 * lane] = (float)first;
+        s.g.low[2 * lane] = (float)(first - (double)(float)first);
+        s.g.high[2 * lane + 1] = (float)sum;
+        s.g.low[2 * lane + 1] = (float)(sum - (double)(float)sum);
         s.g.gam[2 * lane] = exp2f((float)first);
         s.g.gam[2 * lane + 1] = exp2f((float)sum);
         s.g.e[2 * lane] = exp2f((float)(end - first));
@@ -209,7 +211,7 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
             float x[2], y[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
-                const float d = j + c <= i ? exp2f((float)(s.g.G[i] - s.g.G[j + c])) : 0.f;
+                const float d = j + c <= i ? s.g.decay(i, j + c) : 0.f;
                 x[c] = j + c < i ? kk[n][2 * h + c] * d : 0.f;
                 y[c] = qk[n][2 * h + c] * d;
                 s.N[i * ld + j + c] = x[c];
@@ -753,7 +755,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
                 float x[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float d = j + c <= i ? exp2f((float)(s.g.G[i] - s.g.G[j + c])) : 0.f;
+                    const float d = j + c <= i ? s.g.decay(i, j + c) : 0.f;
                     const float f = j + c < i ? -d * dx[n][2 * h + c] : 0.f;
                     x[c] = d * dp[n][2 * h + c];
                     s.tail.F[i * kLdT + j + c] = f;

@@ -26,11 +26,13 @@ __device__ __forceinline__ void st2(__nv_bfloat16 *p, float x, float y)
 }
 
 // Gates of a chunk in scan order, as prepare leaves them for the other kernels.  a is clamped as in the
-// forward kernels; behind the sequence's end a = 1 and b = 0.  The running sums of log2 a are held in 64 bits: a strong
-// decay brings them to several hundred within a chunk, where 32 bits would leave differences of neighbours 1e-5 off.
+// forward kernels; behind the sequence's end a = 1 and b = 0.  The running sums of log2 a are formed in 64 bits and
+// held as two floats, high + low: a strong decay brings them to several hundred within a chunk, where one float would
+// leave differences of neighbours 1e-5 off.
 struct Gates {
-    float gam[kC], e[kC], b[kC], a[kC];
-    double G[kC];
+    float gam[kC], e[kC], b[kC], a[kC], high[kC], low[kC];
+    // D_ij = 2^(G_i - G_j) for j <= i
+    __device__ __forceinline__ float decay(int i, int j) const { return exp2f((high[i] - high[j]) + (low[i] - low[j])); }
 };
 
 // Workspace of one (direction, head, chunk), in bytes.  Tiles are row-major with the 16-byte pieces of a
@@ -219,9 +221,14 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void *src)
 __device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+__device__ __forceinline__ void copy_tile(uint32_t dst, const unsigned char *src, int bytes, int threads)
+{
+    for (int o = threadIdx.x * 16; o < bytes; o += threads * 16) copy16(dst + o, src + o);
+}
+
 __device__ __forceinline__ void copy_block(uint32_t dst, const unsigned char *src, int bytes)
 {
-    for (int o = threadIdx.x * 16; o < bytes; o += blockDim.x * 16) copy16(dst + o, src + o);
+    copy_tile(dst, src, bytes, blockDim.x);
 }
 
 __device__ __forceinline__ float warp_sum(float x)
