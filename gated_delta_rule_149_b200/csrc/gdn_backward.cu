@@ -530,6 +530,270 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
     }
 }
 
+// The same walks with four warps to 16 columns, for calls whose blocks leave SMs idle: the walk's latency is then what
+// counts.  A warp holds a quarter of dk of H^T.  Its partial H^T K^T goes to the others by tokens: warp q adds up tokens
+// 16 q .. 16 q + 15, multiplies them into its part of the triangular product, whose sums by tokens meet the same way,
+// and shares the finished W (or Z) of its tokens as left operands; nothing but the shared operands' loads is done twice.
+// (480p chunk, 16 heads of 74 chunks, dk = dv = 128, bf16: 4.7 us a chunk with pairs of warps.)
+template <int DK, int NI, typename T, int WALK>
+struct StageNarrow {
+    using U = Unit<DK, NI>;
+    static constexpr int head = WALK ? (int)U::size : (int)U::Q;
+    static constexpr int tile = WALK ? NI * kC * 64 : kC * kSlice * (int)sizeof(T);
+    static constexpr int size = head + tile;
+    static constexpr int sums = 16 * 1024, share = 6 * 1024;    // a group's partial sums; its left operands of three terms
+    static constexpr int meet = 2 * (sums + share);
+    static constexpr int buffers = meet + 2 * size <= 227 * 1024 ? 2 : 1;
+    static constexpr int bytes = meet + buffers * size;
+};
+
+template <int DK, int NI, typename T, int WALK>
+__device__ __forceinline__ void chain_narrow(const BwdParams &p, int dir, unsigned char *raw)
+{
+    using U = Unit<DK, NI>;
+    using S = StageNarrow<DK, NI, T, WALK>;
+    constexpr int HK = DK / 4, NT = HK / 8, KS = HK / 16, KP = (int)U::kKey;   // a warp's quarter of dk, its n8 tiles, its k16 steps
+    const int lane = threadIdx.x & 31, me = (threadIdx.x >> 5) & 3, group = threadIdx.x >> 7;
+    const int g = lane >> 2, q2 = 2 * (lane & 3), k0 = me * HK;
+    const int local = blockIdx.y, head = p.head0 + local, sl = blockIdx.x;
+    const int row = 32 * sl + 16 * group;                      // this group's columns of dv: rows of H^T
+    const size_t st = (size_t)p.dk * p.dv;
+    float h[NT][4];
+    const float *init = nullptr;
+    if (WALK == 0 && dir == 0 && p.state_in) init = p.state_in + head * st;
+    if (WALK == 1 && p.dstate) init = p.dstate + ((size_t)dir * p.BH + head) * st;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int kx = k0 + 8 * n + q2 + (x & 1), vx = row + g + 8 * (x >> 1);
+            h[n][x] = init && kx < p.dk ? init[(size_t)kx * p.dv + vx] : 0.f;
+        }
+
+    // sums[a][b][tile][lane]: warp a's part of the first product for warp b's tokens, and then, in the slot that b has
+    // read, b's part of the second product for a's tokens
+    float4 *const sums = reinterpret_cast<float4 *>(raw + group * (S::sums + S::share)) + lane;
+    uint4 *const share = reinterpret_cast<uint4 *>(raw + group * (S::sums + S::share) + S::sums) + lane;   // [tokens / 16][term][lane]
+    auto slot = [&](int a, int b, int tile) -> float4 & { return sums[((a * 4 + b) * 2 + tile) * 32]; };
+    auto barrier = [&] { asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory"); };
+    unsigned char *const stages = raw + S::meet;
+    const uint32_t base = ptx::smem_u32(stages);
+    auto fetch = [&](int step) {
+        const int c = (dir ^ WALK) ? p.nc - 1 - step : step;
+        const size_t ws = ((size_t)dir * p.heads + local) * p.nc + c;
+        const uint32_t dst = base + (step % S::buffers) * S::size;
+        copy_block(dst, p.unit + ws * U::size, S::head);
+        copy_block(dst + S::head, (WALK ? p.ot : p.vt) + (ws * p.slices + sl) * S::tile, S::tile);
+        copy_commit();
+    };
+    auto give = [&](const uint32_t (&a)[3][4]) {
+#pragma unroll
+        for (int x = 0; x < 3; ++x) share[(me * 3 + x) * 32] = make_uint4(a[x][0], a[x][1], a[x][2], a[x][3]);
+    };
+    // h += A X over all tokens, A the shared left operands, X the tile K or Q
+    auto add_outer = [&](uint32_t tX) {
+#pragma unroll
+        for (int k = 0; k < 4; k += 2) {
+            uint32_t a[2][3][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    const uint4 v = share[((k + u) * 3 + x) * 32];
+                    a[u][x][0] = v.x; a[u][x][1] = v.y; a[u][x][2] = v.z; a[u][x][3] = v.w;
+                }
+            uint32_t b[HK / 16][2][NI][4];
+#pragma unroll
+            for (int n = 0; n < HK / 16; ++n)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int x = 0; x < NI; ++x) frag_bt<kKeyRow<DK>>(b[n][u][x], tX + x * KP, 16 * (k + u), k0 + 16 * n);
+            mma_terms<HK / 16, 2, 3, NI>(h, a, b);
+        }
+    };
+
+    if (S::buffers == 2) fetch(0);
+    for (int step = 0; step < p.nc; ++step) {
+        const int c = (dir ^ WALK) ? p.nc - 1 - step : step;
+        const size_t ws = ((size_t)dir * p.heads + local) * p.nc + c;
+        if (S::buffers == 1) {
+            __syncthreads();
+            fetch(step);
+        }
+        copy_wait<0>();
+        __syncthreads();
+        if (S::buffers == 2 && step + 1 < p.nc) fetch(step + 1);   // into the stage that all warps have left
+        const int so = (step % S::buffers) * S::size;
+        const Gates &gt = *reinterpret_cast<const Gates *>(stages + so);
+        const uint32_t tN = base + so + (uint32_t)U::N, tK = base + so + (uint32_t)U::K, tQ = base + so + (uint32_t)U::Q;
+        const uint32_t tP = base + so + (uint32_t)U::P, tX = base + so + S::head;
+        {
+            float *keep = (WALK ? p.GT : p.HT) + (ws * p.dv + row) * DK + k0;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                st2(keep + (size_t)g * DK + 8 * n + q2, h[n][0], h[n][1]);
+                st2(keep + (size_t)(g + 8) * DK + 8 * n + q2, h[n][2], h[n][3]);
+            }
+        }
+        // this warp's part of H^T K^T
+        float r[8][4] = {};
+        {
+            const float one[4] = {1.f, 1.f, 1.f, 1.f};
+            uint32_t a[KS][3][4];
+#pragma unroll
+            for (int k = 0; k < KS; ++k) acc_to_a<3>(a[k], h[2 * k], h[2 * k + 1], one);
+#pragma unroll
+            for (int n = 0; n < 4; n += 2) {
+                uint32_t b[2][KS][NI][4];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int k = 0; k < KS; ++k)
+#pragma unroll
+                        for (int x = 0; x < NI; ++x) frag_b<kKeyRow<DK>>(b[u][k][x], tK + x * KP, k0 + 16 * k, 16 * (n + u));
+                mma_terms<2, KS, 3, NI>(r + 2 * n, a, b);
+            }
+        }
+        const float gend = gt.gam[kC - 1];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) h[n][x] *= gend;
+        auto factors = [&](float (&f)[4], int k, auto of) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) f[x] = of(16 * k + q2 + (x & 1) + 8 * (x >> 1));
+        };
+        if (WALK == 1) {
+            // dU = diag(e) K dH1 + P^T dO, tokens i = 16 k .. feeding tokens j <= i: k = 3 - me here, k = me below, so that the two
+            // triangles together are the same work for every warp; and the terms of diag(gam) dO for Q^T
+#pragma unroll
+            for (int n = 0; n < 8; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) r[n][x] *= gt.e[8 * n + q2 + (x & 1)];
+            uint32_t o[NI][4], a[3][4];
+#pragma unroll
+            for (int x = 0; x < NI; ++x) frag_at<64>(o[x], tX + x * (kC * 64), 16 * group, 16 * (3 - me));
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                if (n > 3 - me) continue;
+                uint32_t b[3][4];
+#pragma unroll
+                for (int x = 0; x < 3; ++x) frag_bt<128>(b[x], tP + x * kTri, 16 * (3 - me), 16 * n);
+                mma_terms(r + 2 * n, o, b);
+            }
+#pragma unroll
+            for (int x = 0; x < NI; ++x) frag_at<64>(o[x], tX + x * (kC * 64), 16 * group, 16 * me);
+            float f[4], u[4] = {}, v[4] = {};
+            factors(f, me, [&](int i) { return gt.gam[i]; });
+#pragma unroll
+            for (int x = NI - 1; x >= 0; --x) {
+                u[0] += lo16(o[x][0]); u[1] += hi16(o[x][0]); u[2] += lo16(o[x][1]); u[3] += hi16(o[x][1]);
+                v[0] += lo16(o[x][2]); v[1] += hi16(o[x][2]); v[2] += lo16(o[x][3]); v[3] += hi16(o[x][3]);
+            }
+            acc_to_a<3>(a, u, v, f);
+            give(a);
+        }
+#pragma unroll
+        for (int n = 0; n < 8; ++n) slot(me, n >> 1, n & 1) = make_float4(r[n][0], r[n][1], r[n][2], r[n][3]);
+        barrier();
+        // R (or dU) of this warp's tokens
+        float rr[2][4], w[2][4];
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const float4 a = slot(0, me, n), b = slot(1, me, n), x = slot(2, me, n), y = slot(3, me, n);
+            rr[n][0] = (a.x + b.x) + (x.x + y.x);
+            rr[n][1] = (a.y + b.y) + (x.y + y.y);
+            rr[n][2] = (a.z + b.z) + (x.z + y.z);
+            rr[n][3] = (a.w + b.w) + (x.w + y.w);
+        }
+        if (WALK == 0) {
+            const unsigned char *vt = stages + so + S::head;
+#pragma unroll
+            for (int n = 0; n < 2; ++n)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int i = 16 * me + 8 * n + q2 + (x & 1), v = 16 * group + g + 8 * (x >> 1);
+                    constexpr int RB = kSlice * sizeof(T), per = 16 / sizeof(T);
+                    rr[n][x] = ldf(reinterpret_cast<const T *>(vt + sw<RB>(i, v / per)) + v % per) - gt.gam[i] * rr[n][x];
+                }
+        }
+        // its part of N diag(b) R for the tokens behind (or N^T diag(b) dU for those before)
+        {
+            float f[4];
+            uint32_t a[3][4];
+            factors(f, me, [&](int i) { return -gt.b[i]; });
+            acc_to_a<3>(a, rr[0], rr[1], f);
+#pragma unroll
+            for (int n = 0; n < 4; ++n) {
+                if (WALK ? n > me : n < me) continue;
+                uint32_t b[3][4];
+#pragma unroll
+                for (int x = 0; x < 3; ++x) {
+                    if (WALK) frag_bt<128>(b[x], tN + x * kTri, 16 * me, 16 * n);
+                    else frag_b<128>(b[x], tN + x * kTri, 16 * me, 16 * n);
+                }
+                float part[2][4] = {};
+                mma_terms(part, a, b);
+                if (n == me) {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) w[x >> 2][x & 3] = rr[x >> 2][x & 3] + part[x >> 2][x & 3];
+                } else {
+                    slot(n, me, 0) = make_float4(part[0][0], part[0][1], part[0][2], part[0][3]);
+                    slot(n, me, 1) = make_float4(part[1][0], part[1][1], part[1][2], part[1][3]);
+                }
+            }
+        }
+        if (WALK == 1) add_outer(tQ);                          // dH += Q^T diag(gam) dO
+        barrier();
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (WALK ? q <= me : q >= me) continue;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float4 y = slot(me, q, n);
+                w[n][0] += y.x;
+                w[n][1] += y.y;
+                w[n][2] += y.z;
+                w[n][3] += y.w;
+            }
+        }
+        {
+            float f[4];
+            uint32_t a[3][4];
+            factors(f, me, [&](int i) { return WALK ? -gt.gam[i] * gt.b[i] : gt.e[i] * gt.b[i]; });
+            acc_to_a<3>(a, w[0], w[1], f);
+            give(a);
+        }
+        barrier();
+        add_outer(tK);                                         // H <- gam_C H + K^T diag(e b) W, or dH <- ... - K^T diag(gam b) Z
+        float *out = (WALK ? p.ZT : p.WT) + (ws * p.dv + row) * kC + 16 * me;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            st2(out + (size_t)g * kC + 8 * n + q2, w[n][0], w[n][1]);
+            st2(out + (size_t)(g + 8) * kC + 8 * n + q2, w[n][2], w[n][3]);
+        }
+    }
+    if (WALK == 1 && dir == 0 && p.dstate_in) {
+        float *to = p.dstate_in + head * st;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int kx = k0 + 8 * n + q2 + (x & 1), vx = row + g + 8 * (x >> 1);
+                if (kx < p.dk) to[(size_t)kx * p.dv + vx] = h[n][x];
+            }
+    }
+}
+
+template <int DK, int NI, typename T>
+__global__ void __launch_bounds__(256, 1) bwd_chain_narrow_kernel(const __grid_constant__ BwdParams p)
+{
+    extern __shared__ __align__(128) unsigned char raw[];
+    if (blockIdx.z < p.dirs) chain_narrow<DK, NI, T, 1>(p, blockIdx.z, raw);
+    else chain_narrow<DK, NI, T, 0>(p, blockIdx.z - p.dirs, raw);
+}
+
 template <int DK, int NI, typename T, int PAIRS>
 __global__ void __launch_bounds__(64 * PAIRS, 1) bwd_chain_kernel(const __grid_constant__ BwdParams p)
 {
@@ -919,12 +1183,15 @@ cudaError_t launch(F kernel, dim3 grid, int threads, size_t smem, const BwdParam
     return err;
 }
 
-template <int DK, int NI, typename T, int PAIRS>
-cudaError_t launch_chains(const BwdParams &p, cudaStream_t stream)
+template <int DK, int NI, typename T>
+cudaError_t launch_chains(const BwdParams &p, bool wide, cudaStream_t stream)
 {
-    constexpr int smem = std::max(Stage<DK, NI, T, 0, PAIRS>::bytes, Stage<DK, NI, T, 1, PAIRS>::bytes);
-    static_assert(smem <= 227 * 1024, "shared memory");
-    return launch(bwd_chain_kernel<DK, NI, T, PAIRS>, dim3((p.slices + PAIRS / 2 - 1) / (PAIRS / 2), p.heads, 2 * p.dirs), 64 * PAIRS,
+    constexpr int kPairs = 4;
+    constexpr int smem = std::max(Stage<DK, NI, T, 0, kPairs>::bytes, Stage<DK, NI, T, 1, kPairs>::bytes);
+    constexpr int narrow = std::max(StageNarrow<DK, NI, T, 0>::bytes, StageNarrow<DK, NI, T, 1>::bytes);
+    static_assert(smem <= 227 * 1024 && narrow <= 227 * 1024, "shared memory");
+    if (!wide) return launch(bwd_chain_narrow_kernel<DK, NI, T>, dim3(p.slices, p.heads, 2 * p.dirs), 256, narrow, p, stream);
+    return launch(bwd_chain_kernel<DK, NI, T, kPairs>, dim3((p.slices + kPairs / 2 - 1) / (kPairs / 2), p.heads, 2 * p.dirs), 64 * kPairs,
                   smem, p, stream);
 }
 
@@ -953,7 +1220,8 @@ cudaError_t run(BwdParams p, cudaStream_t stream)
         p.head0 = h;
         p.heads = std::min(each_pass, p.BH - h);
         const size_t n = (size_t)p.nc * p.dirs * p.heads;
-        // a chain block fills an SM's shared memory: two pairs of warps a block while those blocks fit the SMs
+        // a chain block fills an SM's shared memory: 32 columns a block, four warps to 16 of them, while those blocks fit the
+        // SMs; 64 columns, two warps to 16, beyond
         const bool wide = (long long)p.slices * p.heads * 2 * p.dirs > sms;
         p.unit = ws;
         p.vt = p.unit + n * U::size;
@@ -964,7 +1232,7 @@ cudaError_t run(BwdParams p, cudaStream_t stream)
         p.ZT = p.WT + n * p.dv * kC;
         err = launch(bwd_prepare_kernel<DK, NI, T>, dim3(p.nc, p.heads, p.dirs), kPrepThreads, sizeof(PrepSmem<DK, NI>), p, stream);
         if (err == cudaSuccess)
-            err = wide ? launch_chains<DK, NI, T, 4>(p, stream) : launch_chains<DK, NI, T, 2>(p, stream);
+            err = launch_chains<DK, NI, T>(p, wide, stream);
         if (err == cudaSuccess) {
             if constexpr (DK == 128 && NI == 1) err = launch_grad_tc(p, stream);
             else err = launch(bwd_grad_kernel<DK, NI, T>, dim3(p.nc, p.heads), kGradThreads, sizeof(GradSmem<DK, NI>), p, stream);
