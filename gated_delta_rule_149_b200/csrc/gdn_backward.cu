@@ -42,6 +42,7 @@
 #include <cstdint>
 
 #include "gdn_backward.cuh"
+#include "gdn_chunk_common.cuh"
 
 namespace gdn {
 namespace {
@@ -273,6 +274,32 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
 // triangular product being the only one that is done twice.  One warp per 16 columns would spare that, but takes
 // 8.9 us for a chunk of 64 tokens (dk = dv = 128, bf16): a walk is bound by its own latency, and the pair shortens it.
 
+// A stage's two bulk copies, issued by one thread (sixteen-byte copies by all threads took 1000 of a chunk's 7300 cycles)
+// and awaited by all.
+struct Loads {
+    uint64_t bar[2];
+    int abort;
+    __device__ __forceinline__ void init()
+    {
+        if (threadIdx.x == 0) {
+            mbar_init(&bar[0], 1);
+            mbar_init(&bar[1], 1);
+            abort = 0;
+            fence_mbar_init();
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ void fetch(unsigned char *to, const unsigned char *unit, int head, const unsigned char *tile, int bytes, int b)
+    {
+        if (threadIdx.x) return;
+        fence_proxy_async_smem();                              // behind the reads of what the stage held
+        mbar_arrive_expect_tx(&bar[b], head + bytes);
+        bulk_load(to, unit, head, &bar[b]);
+        bulk_load(to + head, tile, bytes, &bar[b]);
+    }
+    __device__ __forceinline__ bool wait(int b, uint32_t parity, int *err) { return wait_bar(&bar[b], parity, &abort, err, 128); }
+};
+
 // bytes of one stage: the unit's tiles from its start (forward: gates, N, K; backward: all) and V or dO
 template <int DK, int NI, typename T, int WALK, int PAIRS>
 struct Stage {
@@ -337,14 +364,13 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
     float4 *const mine = reinterpret_cast<float4 *>(raw) + (pair * 2 + half) * 256 + lane;
     const float4 *const other = reinterpret_cast<const float4 *>(raw) + (pair * 2 + 1 - half) * 256 + lane;
     unsigned char *const stages = raw + S::meet;
+    __shared__ Loads loads;
     const uint32_t base = ptx::smem_u32(stages);
     auto fetch = [&](int step) {
         const int c = (dir ^ WALK) ? p.nc - 1 - step : step;
         const size_t ws = ((size_t)dir * p.heads + local) * p.nc + c;
-        const uint32_t dst = base + (step % S::buffers) * S::size;
-        copy_block(dst, p.unit + ws * U::size, S::head);
-        copy_block(dst + S::head, (WALK ? p.ot : p.vt) + (ws * p.slices + sl) * S::tile, tiles);
-        copy_commit();
+        loads.fetch(stages + (step % S::buffers) * S::size, p.unit + ws * U::size, S::head,
+                    (WALK ? p.ot : p.vt) + (ws * p.slices + sl) * S::tile, tiles, step % S::buffers);
     };
     // r (16 x 64, columns tokens) += the warp's part of H^T K^T
     auto state_times_keys = [&](float (&r)[8][4], uint32_t tK) {
@@ -394,6 +420,7 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
         }
     };
 
+    loads.init();
     if (S::buffers == 2) fetch(0);
     for (int step = 0; step < p.nc; ++step) {
         const int c = (dir ^ WALK) ? p.nc - 1 - step : step;
@@ -402,8 +429,8 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
             __syncthreads();
             fetch(step);
         }
-        copy_wait<0>();
-        __syncthreads();
+        const bool ok = loads.wait(step % S::buffers, step / S::buffers & 1, p.err);
+        if (__syncthreads_or(!ok)) return;
         if (S::buffers == 2 && step + 1 < p.nc) fetch(step + 1);   // into the stage that all warps have left
         if (!on) continue;
         const int so = (step % S::buffers) * S::size;
@@ -577,14 +604,13 @@ __device__ __forceinline__ void chain_narrow(const BwdParams &p, int dir, unsign
     auto slot = [&](int a, int b, int tile) -> float4 & { return sums[((a * 4 + b) * 2 + tile) * 32]; };
     auto barrier = [&] { asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory"); };
     unsigned char *const stages = raw + S::meet;
+    __shared__ Loads loads;
     const uint32_t base = ptx::smem_u32(stages);
     auto fetch = [&](int step) {
         const int c = (dir ^ WALK) ? p.nc - 1 - step : step;
         const size_t ws = ((size_t)dir * p.heads + local) * p.nc + c;
-        const uint32_t dst = base + (step % S::buffers) * S::size;
-        copy_block(dst, p.unit + ws * U::size, S::head);
-        copy_block(dst + S::head, (WALK ? p.ot : p.vt) + (ws * p.slices + sl) * S::tile, S::tile);
-        copy_commit();
+        loads.fetch(stages + (step % S::buffers) * S::size, p.unit + ws * U::size, S::head,
+                    (WALK ? p.ot : p.vt) + (ws * p.slices + sl) * S::tile, S::tile, step % S::buffers);
     };
     auto give = [&](const uint32_t (&a)[3][4]) {
 #pragma unroll
@@ -613,6 +639,7 @@ __device__ __forceinline__ void chain_narrow(const BwdParams &p, int dir, unsign
         }
     };
 
+    loads.init();
     if (S::buffers == 2) fetch(0);
     for (int step = 0; step < p.nc; ++step) {
         const int c = (dir ^ WALK) ? p.nc - 1 - step : step;
@@ -621,8 +648,8 @@ __device__ __forceinline__ void chain_narrow(const BwdParams &p, int dir, unsign
             __syncthreads();
             fetch(step);
         }
-        copy_wait<0>();
-        __syncthreads();
+        const bool ok = loads.wait(step % S::buffers, step / S::buffers & 1, p.err);
+        if (__syncthreads_or(!ok)) return;
         if (S::buffers == 2 && step + 1 < p.nc) fetch(step + 1);   // into the stage that all warps have left
         const int so = (step % S::buffers) * S::size;
         const Gates &gt = *reinterpret_cast<const Gates *>(stages + so);
@@ -1213,6 +1240,7 @@ cudaError_t run(BwdParams p, cudaStream_t stream)
     int dev = 0, sms = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (err == cudaSuccess) err = device_error_word(&p.err);
     unsigned char *ws = nullptr;
     if (err == cudaSuccess) err = ws_alloc(reinterpret_cast<void **>(&ws), per_head * each_pass, stream);
     if (err != cudaSuccess) return err;
@@ -1250,7 +1278,7 @@ cudaError_t launch_backward(const BwdArgs &a, cudaStream_t stream)
     p.q = a.f.q; p.k = a.f.k; p.v = a.f.v; p.dout = a.dout;
     p.beta = a.f.beta; p.decay = a.f.decay; p.state_in = a.f.state_in; p.dstate = a.dstate;
     p.dq = a.dq; p.dk_ = a.dk; p.dv_ = a.dv; p.dbeta = a.dbeta; p.ddecay = a.ddecay; p.dstate_in = a.dstate_in;
-    p.BH = a.f.B * a.f.H; p.T = a.f.T; p.nc = (a.f.T + kC - 1) / kC; p.dk = a.f.dk; p.dv = a.f.dv;
+    p.BH = a.f.B * a.f.H; p.T = a.f.T; p.nc = (a.f.T + bwd::kC - 1) / bwd::kC; p.dk = a.f.dk; p.dv = a.f.dv;
     p.dirs = a.f.bidi ? 2 : 1;
     if (a.f.fp32) return p.dk <= 64 ? run<64, 3, float>(p, stream) : run<128, 3, float>(p, stream);
     return p.dk <= 64 ? run<64, 1, __nv_bfloat16>(p, stream) : run<128, 1, __nv_bfloat16>(p, stream);

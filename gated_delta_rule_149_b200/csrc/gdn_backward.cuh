@@ -62,6 +62,7 @@ struct BwdParams {
     float *WT, *ZT;            // [dv][64 tokens]
     int head0, heads;          // the heads [head0, head0 + heads) of B*H
     int BH, T, nc, dk, dv, dirs, slices;
+    int *err;                  // the device error word of bounded waits
 };
 
 // A chunk of one scan: its tokens in scan order.  Chunks are tiles [64 c, 64 c + n) of the sequence for

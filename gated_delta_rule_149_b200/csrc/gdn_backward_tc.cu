@@ -191,7 +191,7 @@ __device__ __forceinline__ void issue_tail(uint32_t tmem, uint32_t base)
 }
 
 // The products of every chunk of this block, as the workers hand their operands over.
-__device__ __forceinline__ void issuer(const BwdParams &p, Smem::Small &s, uint32_t tmem, uint32_t base, int *err)
+__device__ __forceinline__ void issuer(const BwdParams &p, Smem::Small &s, uint32_t tmem, uint32_t base)
 {
     uint32_t phase[3] = {0, 0, 0};
     const int steps = p.dv / kRows;
@@ -199,13 +199,13 @@ __device__ __forceinline__ void issuer(const BwdParams &p, Smem::Small &s, uint3
         for (int dir = 0; dir < p.dirs; ++dir) {
             for (int step = 0; step < steps; ++step) {
                 const int b = step & 1;
-                if (!wait_bar(&s.full[b], phase[b], &s.abort, err, 64)) return;
+                if (!wait_bar(&s.full[b], phase[b], &s.abort, p.err, 64)) return;
                 phase[b] ^= 1;
                 tc_fence_after();
                 issue_step(tmem, base, Smem::buf + b * kBuf, step);
                 mma_commit(&s.done[b]);
             }
-            if (!wait_bar(&s.full[2], phase[2], &s.abort, err, 64)) return;
+            if (!wait_bar(&s.full[2], phase[2], &s.abort, p.err, 64)) return;
             phase[2] ^= 1;
             tc_fence_after();
             issue_tail(tmem, base);
@@ -223,7 +223,7 @@ __device__ __forceinline__ void hand_over(uint64_t *bar)
 }
 
 template <bool BIDI>
-__device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint32_t tmem, unsigned char *sm, int *err)
+__device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint32_t tmem, unsigned char *sm)
 {
     const uint32_t base = smem_u32(sm);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -279,7 +279,7 @@ __device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint
                 now = next;
                 if (step + 1 < steps) fetch(next, step + 1);
                 if (step >= 2) {
-                    ok = ok && wait_bar(&s.done[b], phase[b], &s.abort, err, 64);
+                    ok = ok && wait_bar(&s.done[b], phase[b], &s.abort, p.err, 64);
                     phase[b] ^= 1;
                 }
 #pragma unroll
@@ -318,7 +318,7 @@ __device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint
 #pragma unroll
             for (int b = 0; b < 2; ++b)
                 if (steps > b) {
-                    ok = ok && wait_bar(&s.done[b], phase[b], &s.abort, err, 64);
+                    ok = ok && wait_bar(&s.done[b], phase[b], &s.abort, p.err, 64);
                     phase[b] ^= 1;
                 }
             tc_fence_after();
@@ -469,7 +469,7 @@ __device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint
                     s.db[tok] += b;
                 }
             }
-            ok = ok && wait_bar(&s.done[2], phase[2], &s.abort, err, 64);
+            ok = ok && wait_bar(&s.done[2], phase[2], &s.abort, p.err, 64);
             phase[2] ^= 1;
             tc_fence_after();
             ok = !named_bar_any(1, kWorkers, !ok);
@@ -538,7 +538,7 @@ __device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint
 }
 
 template <bool BIDI>
-__global__ void __launch_bounds__(kThreads, 1) bwd_grad_tc_kernel(const __grid_constant__ BwdParams p, int *err)
+__global__ void __launch_bounds__(kThreads, 1) bwd_grad_tc_kernel(const __grid_constant__ BwdParams p)
 {
     extern __shared__ unsigned char dyn[];
     unsigned char *const sm = reinterpret_cast<unsigned char *>((reinterpret_cast<uintptr_t>(dyn) + 1023) & ~(uintptr_t)1023);
@@ -560,8 +560,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_grad_tc_kernel(const __grid_c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = s.tmem;
-    if (tid < kWorkers) workers<BIDI>(p, s, tmem, sm, err);
-    else if (tid == kWorkers) issuer(p, s, tmem, smem_u32(sm), err);
+    if (tid < kWorkers) workers<BIDI>(p, s, tmem, sm);
+    else if (tid == kWorkers) issuer(p, s, tmem, smem_u32(sm));
     __syncwarp();
     tc_fence_before();
     __syncthreads();
@@ -577,10 +577,8 @@ namespace bwd {
 
 cudaError_t launch_grad_tc(const BwdParams &p, cudaStream_t stream)
 {
-    int *word = nullptr;
-    cudaError_t err = device_error_word(&word);
     auto *kernel = p.dirs == 2 ? bwd_grad_tc_kernel<true> : bwd_grad_tc_kernel<false>;
-    if (err == cudaSuccess) err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::bytes);
+    cudaError_t err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem::bytes);
     if (err != cudaSuccess) return err;
     // a block fills an SM (shared and tensor memory): one for each, walking the chunks
     int dev = 0, sms = 0;
@@ -588,7 +586,7 @@ cudaError_t launch_grad_tc(const BwdParams &p, cudaStream_t stream)
     if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess) return err;
     const long long units = (long long)p.nc * p.heads;
-    kernel<<<(unsigned)(units < sms ? units : sms), kThreads, Smem::bytes, stream>>>(p, word);
+    kernel<<<(unsigned)(units < sms ? units : sms), kThreads, Smem::bytes, stream>>>(p);
     err = cudaGetLastError();
     if (err == cudaSuccess) count_launches(1);
     return err;
