@@ -53,10 +53,18 @@ using namespace bwd;
 // Grid (chunks, heads, directions), 256 threads.
 template <int DK, int NI>
 struct PrepSmem {
-    unsigned char K[NI * Unit<DK, NI>::kKey];
-    unsigned char Q[NI * Unit<DK, NI>::kKey];
-    float X[kC * (kC + 4)];        // X diag(b)
-    float N[kC * (kC + 4)];
+    struct Keys {
+        unsigned char K[NI * Unit<DK, NI>::kKey];
+        unsigned char Q[NI * Unit<DK, NI>::kKey];
+    };
+    struct Solve {
+        float X[kC * (kC + 4)];    // X diag(b)
+        float N[kC * (kC + 4)];
+    };
+    union {                        // K and Q are done with when X is there: small blocks, four to an SM
+        Keys k;
+        Solve n;
+    };
     Gates g;
 };
 
@@ -106,7 +114,7 @@ __device__ __forceinline__ void get8(const T *row, bool on, int c, int len, floa
 }
 
 template <int DK, int NI, typename T>
-__global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_constant__ BwdParams p)
+__global__ void __launch_bounds__(kPrepThreads, NI == 1 ? 4 : 1) bwd_prepare_kernel(const __grid_constant__ BwdParams p)
 {
     extern __shared__ __align__(128) unsigned char raw[];
     using U = Unit<DK, NI>;
@@ -155,9 +163,9 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
         const size_t row = on ? (size_t)t.tok(i) * p.dk : 0;
         float x[8];
         get8(kb + row, on, 8 * c, p.dk, x);
-        put8<NI, kKeyRow<DK>, T>(x, i, c, s.K, unit + U::K, U::kKey);
+        put8<NI, kKeyRow<DK>, T>(x, i, c, s.k.K, unit + U::K, U::kKey);
         get8(qb + row, on, 8 * c, p.dk, x);
-        put8<NI, kKeyRow<DK>, T>(x, i, c, s.Q, unit + U::Q, U::kKey);
+        put8<NI, kKeyRow<DK>, T>(x, i, c, s.k.Q, unit + U::Q, U::kKey);
     }
     const T *vb = static_cast<const T *>(p.v) + (size_t)t.head * p.T * p.dv;
     const T *ob = static_cast<const T *>(p.dout) + (size_t)t.head * p.T * p.dv;
@@ -183,7 +191,7 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
 
     // K K^T and Q K^T: warp w has rows 16 (w % 4) .. and columns 32 (w / 4) .., lower triangle only
     const int wm = warp & 3, wn = warp >> 2;
-    const uint32_t ks = ptx::smem_u32(s.K), qs = ptx::smem_u32(s.Q);
+    const uint32_t ks = ptx::smem_u32(s.k.K), qs = ptx::smem_u32(s.k.Q);
     float kk[4][4] = {}, qk[4][4] = {};
 #pragma unroll 2
     for (int k = 0; k < DK; k += 16) {
@@ -204,6 +212,7 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
             mma_terms(qk + 2 * n, qa, b);
         }
     }
+    __syncthreads();
 #pragma unroll
     for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -215,8 +224,8 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
                 const float d = j + c <= i ? s.g.decay(i, j + c) : 0.f;
                 x[c] = j + c < i ? kk[n][2 * h + c] * d : 0.f;
                 y[c] = qk[n][2 * h + c] * d;
-                s.N[i * ld + j + c] = x[c];
-                s.X[i * ld + j + c] = x[c] * s.g.b[j + c];
+                s.n.N[i * ld + j + c] = x[c];
+                s.n.X[i * ld + j + c] = x[c] * s.g.b[j + c];
             }
             uint32_t u[3];
             split2<3>(y[0], y[1], u);
@@ -230,20 +239,20 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
     for (int r = 0; r < kC; r += 16) {
         if (r) {
             const int i = r + (tid >> 4), j = 4 * (tid & 15);
-            float4 y = *reinterpret_cast<float4 *>(&s.N[i * ld + j]);
+            float4 y = *reinterpret_cast<float4 *>(&s.n.N[i * ld + j]);
             for (int l = 0; l < r; l += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(&s.X[i * ld + l]);
+                const float4 x = *reinterpret_cast<const float4 *>(&s.n.X[i * ld + l]);
                 const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const float4 n = *reinterpret_cast<const float4 *>(&s.N[(l + u) * ld + j]);
+                    const float4 n = *reinterpret_cast<const float4 *>(&s.n.N[(l + u) * ld + j]);
                     y.x = fmaf(-xs[u], n.x, y.x);
                     y.y = fmaf(-xs[u], n.y, y.y);
                     y.z = fmaf(-xs[u], n.z, y.z);
                     y.w = fmaf(-xs[u], n.w, y.w);
                 }
             }
-            *reinterpret_cast<float4 *>(&s.N[i * ld + j]) = y;
+            *reinterpret_cast<float4 *>(&s.n.N[i * ld + j]) = y;
             __syncthreads();
         }
         if (tid < kC) {
@@ -251,10 +260,10 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
             float y[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                y[i] = s.N[(r + i) * ld + j];
+                y[i] = s.n.N[(r + i) * ld + j];
 #pragma unroll
-                for (int l = 0; l < i; ++l) y[i] = fmaf(-s.X[(r + i) * ld + r + l], y[l], y[i]);
-                s.N[(r + i) * ld + j] = y[i];
+                for (int l = 0; l < i; ++l) y[i] = fmaf(-s.n.X[(r + i) * ld + r + l], y[l], y[i]);
+                s.n.N[(r + i) * ld + j] = y[i];
             }
         }
         __syncthreads();
@@ -263,7 +272,7 @@ __global__ void __launch_bounds__(kPrepThreads) bwd_prepare_kernel(const __grid_
         const int i = e / (kC / 8), c = e % (kC / 8);
         float x[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) x[u] = s.N[i * ld + 8 * c + u];
+        for (int u = 0; u < 8; ++u) x[u] = s.n.N[i * ld + 8 * c + u];
         put8<3, 128, T>(x, i, c, nullptr, unit + U::N, kTri);
     }
 }
