@@ -161,7 +161,7 @@ __device__ __forceinline__ float row_sum(float x)
 // Grid (token tiles, head splits, batches).  LPR lanes hold a row; a block's threads are LPR x tokens x the rest,
 // which walks the rows (heads of q, then of k).
 template <typename T, bool HALF, bool VEC, int LPR, bool L2, bool BACK>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotParams p)
+__global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotParams p)
 {
     extern __shared__ float2 cs[];                    // [tokens][d/2]: cosine, sine
     const int pairs = p.d / 2, t0 = blockIdx.x * p.tokens, b = blockIdx.z;
