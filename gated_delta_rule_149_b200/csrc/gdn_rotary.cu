@@ -27,12 +27,13 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxPairs = 128;
 constexpr int kPer = 8;            // pairs per thread
+constexpr int kMaxTokens = 16;     // tokens per block
 
 struct RotParams {
     View x[2], g[2], y[2];
     const int *positions;
     long long pos_sb;
-    double freq[kMaxPairs];        // turns per position, by pair
+    double slope[3], slope_lo[3];  // log2 of the i-th frequency of an axis is i (slope + slope_lo)
     int end_t, end_h;              // pairs below end_t: time; below end_h: height; the others: width
     int H, T, d, rows;             // rows: heads of q and k together
     int tokens;                    // tokens per block
@@ -164,19 +165,31 @@ template <typename T, bool HALF, bool VEC, int LPR, bool L2, bool BACK>
 __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_constant__ RotParams p)
 {
     extern __shared__ float2 cs[];                    // [tokens][d/2]: cosine, sine
+    __shared__ double at[kMaxTokens][3], freq[kMaxPairs];
     const int pairs = p.d / 2, t0 = blockIdx.x * p.tokens, b = blockIdx.z;
-    for (int e = threadIdx.x; e < p.tokens * pairs; e += kThreads) {
-        const int t = t0 + e / pairs, q = e % pairs;
-        if (t >= p.T) break;
-        const int axis = q < p.end_t ? 0 : q < p.end_h ? 1 : 2;
-        double at;
+    // the frequencies, in turns per position (formed here: as a table in the kernel's arguments they cost every block a
+    // string of constant-cache misses), and the tokens' positions
+    if (threadIdx.x < pairs) {
+        const int q = threadIdx.x, axis = q < p.end_t ? 0 : q < p.end_h ? 1 : 2;
+        const double i = q - (axis == 0 ? 0 : axis == 1 ? p.end_t : p.end_h);
+        freq[q] = exp2(i * p.slope[axis]) * fma(i * p.slope_lo[axis], 0.693147180559945309, 1.0) * 0.159154943091895336;
+    } else if (threadIdx.x >= kMaxPairs && threadIdx.x - kMaxPairs < p.tokens && t0 + (int)threadIdx.x - kMaxPairs < p.T) {
+        const int tl = threadIdx.x - kMaxPairs, t = t0 + tl;
         if (p.positions) {
-            at = (double)p.positions[b * p.pos_sb + (long long)t * 3 + axis];
+#pragma unroll
+            for (int i = 0; i < 3; ++i) at[tl][i] = (double)p.positions[b * p.pos_sb + (long long)t * 3 + i];
         } else {
-            const long long n = p.start + t, row = n / p.grid_w;
-            at = (double)(axis == 0 ? row / p.grid_h : axis == 1 ? row % p.grid_h : n % p.grid_w);
+            const long long n = p.start + t, row = n / p.grid_w, frame = row / p.grid_h;
+            at[tl][0] = (double)frame;
+            at[tl][1] = (double)(row - frame * p.grid_h);
+            at[tl][2] = (double)(n - row * p.grid_w);
         }
-        const double turns = at * p.freq[q];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.tokens * pairs; e += kThreads) {
+        const int tl = e / pairs, q = e - tl * pairs;
+        if (t0 + tl >= p.T) break;
+        const double turns = at[tl][q < p.end_t ? 0 : q < p.end_h ? 1 : 2] * freq[q];
         float s, c;
         sincospif(2.f * (float)(turns - rint(turns)), &s, &c);
         cs[e] = make_float2(c, s);
@@ -199,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 4) rotary_kernel(const __grid_consta
     }
     // every lane takes every step, so that the row sums see whole warps
     const int rounds = (p.rows + step - 1) / step;
-#pragma unroll 2
+#pragma unroll 1
     for (int k = 0; k < rounds; ++k) {
         const int r = first + k * step;
         const bool act = on && r < p.rows;
@@ -307,16 +320,13 @@ cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t stream)
     }
     p.positions = a.positions;
     p.pos_sb = a.pos_sb;
-    double *f = p.freq;
-    for (int n : a.axes) {
-        // theta^(-2 i / n) for i = 8 u + v as a product of two powers: a quarter of the calls of pow, which would
-        // otherwise be most of the host's time
-        double low[8];
-        for (int v = 0; v < 8 && 2 * v < n; ++v) low[v] = std::pow(a.theta, -2.0 * v / n);
-        for (int i = 0; 2 * i < n; i += 8) {
-            const double high = std::pow(a.theta, -2.0 * i / n) / 6.283185307179586476925;
-            for (int v = 0; v < 8 && 2 * (i + v) < n; ++v) *f++ = high * low[v];
-        }
+    // theta^(-2 i / n): the slope's first part has 40 bits, so that its multiples are exact
+    for (int x = 0; x < 3; ++x) {
+        const long double slope = a.axes[x] ? -2.0L * std::log2((long double)a.theta) / a.axes[x] : 0.0L;
+        int e = 0;
+        const double m = std::frexp((double)slope, &e);
+        p.slope[x] = std::ldexp(std::rint(std::ldexp(m, 40)), e - 40);
+        p.slope_lo[x] = (double)(slope - p.slope[x]);
     }
     p.end_t = a.axes[0] / 2;
     p.end_h = p.end_t + a.axes[1] / 2;
@@ -324,12 +334,15 @@ cudaError_t launch_rotary(const RotaryArgs &a, cudaStream_t stream)
     p.grid_h = a.grid_h; p.grid_w = a.grid_w; p.start = a.start; p.eps = a.eps;
     int lanes = vec ? 2 : 16;
     while (lanes * 2 * kPer < a.d) lanes *= 2;
-    p.tokens = 8;
     int dev = 0, sms = 0;
     cudaError_t err = cudaGetDevice(&dev);
     if (err == cudaSuccess) err = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
     if (err != cudaSuccess) return err;
-    // a short sequence leaves SMs idle: its heads are split over blocks as well
+    // 16 tokens a block where that leaves every SM eight blocks (720p clip, backward: 611 us; 14 more with 8), else 8 (480p
+    // chunk: 20.5 us; 2 more with 16)
+    p.tokens = (long long)((a.T + 15) / 16) * a.B >= 8LL * sms ? 16 : 8;
+    // a short sequence leaves SMs idle: its heads are split over blocks as well, though each forms the sines again (the
+    // 480p chunk, which fills the SMs, takes 20.5 us unsplit, 22.7 in two)
     const long long tiles = (a.T + p.tokens - 1) / p.tokens;
     const int side = kThreads / lanes / p.tokens, most = (p.rows + side - 1) / side;
     int splits = 1;
