@@ -279,8 +279,8 @@ __global__ void __launch_bounds__(kPrepThreads, NI == 1 ? 4 : 1) bwd_prepare_ker
 
 // ---------------------------------------------------------------- chains
 // Grid (groups of 16 PAIRS columns of dv, heads, directions and walks).  A pair of warps carries 16 columns: each holds
-// half of dk of H^T, their partial H^T K^T meet in shared memory, and both go on with the whole of W (or Z), the
-// triangular product being the only one that is done twice.  One warp per 16 columns would spare that, but takes
+// half of dk of H^T; their partial H^T K^T meet in shared memory, and again their halves of the triangular product, and
+// both go on with the whole of W (or Z).  One warp per 16 columns would spare that, but takes
 // 8.9 us for a chunk of 64 tokens (dk = dv = 128, bf16): a walk is bound by its own latency, and the pair shortens it.
 
 // A stage's two bulk copies, issued by one thread (sixteen-byte copies by all threads took 1000 of a chunk's 7300 cycles)
@@ -370,8 +370,7 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
             h[n][x] = init && on && kx < p.dk ? init[(size_t)kx * p.dv + vx] : 0.f;
         }
 
-    float4 *const mine = reinterpret_cast<float4 *>(raw) + (pair * 2 + half) * 256 + lane;
-    const float4 *const other = reinterpret_cast<const float4 *>(raw) + (pair * 2 + 1 - half) * 256 + lane;
+    float4 *const meets = reinterpret_cast<float4 *>(raw) + pair * 512 + lane;
     unsigned char *const stages = raw + S::meet;
     __shared__ Loads loads;
     const uint32_t base = ptx::smem_u32(stages);
@@ -414,14 +413,17 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
             mma_terms<2, 2, 3, NI>(h + 2 * n, a, b);
         }
     };
-    // adds the other warp's part of r to this one's
-    auto meet = [&](float (&r)[8][4]) {
+    // adds the other warp's part of r to this one's.  The first exchange writes the warp's own room and reads the other's, the
+    // second the other way round: what a warp overwrites it has read itself
+    auto meet = [&](float (&r)[8][4], int second) {
+        float4 *const to = meets + (half ^ second) * 256;
+        const float4 *const from = meets + (half ^ second ^ 1) * 256;
 #pragma unroll
-        for (int n = 0; n < 8; ++n) mine[32 * n] = make_float4(r[n][0], r[n][1], r[n][2], r[n][3]);
+        for (int n = 0; n < 8; ++n) to[32 * n] = make_float4(r[n][0], r[n][1], r[n][2], r[n][3]);
         asm volatile("bar.sync %0, 64;" ::"r"(pair + 1) : "memory");
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
-            const float4 y = other[32 * n];
+            const float4 y = from[32 * n];
             r[n][0] += y.x;
             r[n][1] += y.y;
             r[n][2] += y.z;
@@ -466,7 +468,7 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
             for (int x = 0; x < 4; ++x) f[x] = of(16 * k + q2 + (x & 1) + 8 * (x >> 1));
         };
         if (WALK == 0) {
-            meet(r);
+            meet(r, 0);
             // R = V - gam (H^T K^T)
             const unsigned char *vt = stages + so + S::head + (pair >> 1) * S::tile;
 #pragma unroll
@@ -477,11 +479,12 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
                     constexpr int RB = kSlice * sizeof(T), per = 16 / sizeof(T);
                     const float y = ldf(reinterpret_cast<const T *>(vt + sw<RB>(i, v / per)) + v % per);
                     r[n][x] = y - gt.gam[i] * r[n][x];
-                    w[n][x] = r[n][x];
+                    w[n][x] = half ? 0.f : r[n][x];
                 }
-            // W = R - N diag(b) R: tokens j = 16 k .. feed tokens i >= j
+            // W = R - N diag(b) R: tokens j = 16 k .. feed tokens i >= j; the warps take two k each
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
+                if ((k == 0 || k == 3) != (half == 0)) continue;
                 float f[4];
                 uint32_t a[3][4];
                 factors(f, k, [&](int i) { return -gt.b[i]; });
@@ -519,14 +522,15 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
                 }
                 add_outer(a, tQ, k);
             }
-            meet(r);
-            // Z = dU - N^T diag(b) dU: tokens i = 16 k .. feed tokens j <= i
+            meet(r, 0);
+            // Z = dU - N^T diag(b) dU: tokens i = 16 k .. feed tokens j <= i; the warps take two k each
 #pragma unroll
             for (int n = 0; n < 8; ++n)
 #pragma unroll
-                for (int x = 0; x < 4; ++x) w[n][x] = r[n][x];
+                for (int x = 0; x < 4; ++x) w[n][x] = half ? 0.f : r[n][x];
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
+                if ((k == 0 || k == 3) != (half == 0)) continue;
                 float f[4];
                 uint32_t a[3][4];
                 factors(f, k, [&](int i) { return -gt.b[i]; });
@@ -534,6 +538,7 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
                 triangle<true>(w, a, tN, k, 0, k + 1);
             }
         }
+        meet(w, 1);
         float *out = (WALK ? p.ZT : p.WT) + (ws * p.dv + row) * kC;
 #pragma unroll
         for (int n = 0; n < 8; ++n) {
