@@ -5,6 +5,7 @@
 // record), and every argument error is caught before anything is launched.
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cstdarg>
 #include <cstdint>
 #include <cstdio>
@@ -456,6 +457,7 @@ int gdn_backward(const void *q, const void *k, const void *v, const float *beta,
         for (const void *p : ptrs)
             if (misaligned(p)) return fail(GDN_ERR_MISALIGNED, "a gradient output is not 16-byte aligned");
         if (misaligned(dstate_in)) return fail(GDN_ERR_MISALIGNED, "dstate_in is not 16-byte aligned");
+        if (T > INT_MAX - 64) return fail(GDN_ERR_UNSUPPORTED, "T = %d is too long", T);
         if (mode & GDN_RECURRENT)
             return fail(GDN_ERR_UNSUPPORTED, "gdn_backward has one form for every size (no GDN_RECURRENT)");
         gdn::BwdArgs a;
@@ -488,6 +490,7 @@ int gdn_debug_wait_limit(unsigned long long ns)
     const unsigned long long v = ns ? ns : 4000000000ull;
     cudaError_t e = gdn::set_wait_limit_pool(v);
     if (e == cudaSuccess) e = gdn::set_wait_limit_tc(v);
+    if (e == cudaSuccess) e = gdn::set_wait_limit_backward(v);
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "wait limit: %s", cudaGetErrorString(e));
     return ok();
 }

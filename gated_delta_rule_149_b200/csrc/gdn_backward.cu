@@ -223,7 +223,7 @@ __global__ void __launch_bounds__(kPrepThreads, NI == 1 ? 4 : 1) bwd_prepare_ker
             for (int c = 0; c < 2; ++c) {
                 const float d = j + c <= i ? s.g.decay(i, j + c) : 0.f;
                 x[c] = j + c < i ? kk[n][2 * h + c] * d : 0.f;
-                y[c] = qk[n][2 * h + c] * d;
+                y[c] = j + c <= i ? qk[n][2 * h + c] * d : 0.f;
                 s.n.N[i * ld + j + c] = x[c];
                 s.n.X[i * ld + j + c] = x[c] * s.g.b[j + c];
             }
@@ -1062,7 +1062,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
                 for (int c = 0; c < 2; ++c) {
                     const float d = j + c <= i ? s.g.decay(i, j + c) : 0.f;
                     const float f = j + c < i ? -d * dx[n][2 * h + c] : 0.f;
-                    x[c] = d * dp[n][2 * h + c];
+                    x[c] = j + c <= i ? d * dp[n][2 * h + c] : 0.f;
                     s.tail.F[i * kLdT + j + c] = f;
                     s.tail.M[i * (kC + 1) + j + c] = j + c < i ? f * kk[n][2 * h + c] + x[c] * qk[n][2 * h + c] : 0.f;
                 }
@@ -1285,6 +1285,12 @@ cudaError_t run(BwdParams p, cudaStream_t stream)
 }
 
 }  // namespace
+
+cudaError_t set_wait_limit_backward(unsigned long long ns)
+{
+    const cudaError_t err = set_module_wait_limit(ns);
+    return err == cudaSuccess ? bwd::set_wait_limit_tc(ns) : err;
+}
 
 cudaError_t launch_backward(const BwdArgs &a, cudaStream_t stream)
 {

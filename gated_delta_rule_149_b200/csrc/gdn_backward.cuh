@@ -265,6 +265,7 @@ __device__ __forceinline__ void get8f(const float *p, float (&x)[8])
 
 // The gradients kernel for bf16, dk of 96 or 128: on tcgen05 tensor cores (gdn_backward_tc.cu).
 cudaError_t launch_grad_tc(const BwdParams &p, cudaStream_t stream);
+cudaError_t set_wait_limit_tc(unsigned long long ns);   // of this kernel's module
 
 }  // namespace bwd
 }  // namespace gdn

@@ -396,7 +396,7 @@ __device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint
                     qk[i] = xQ[(8 * group + i) ^ lane];
                 }
                 const float dc = j <= ti ? s.g.decay(ti, j) : 0.f;
-                const float x = dc * (pp[i] + xP[ti]);                                   // E
+                const float x = j <= ti ? dc * (pp[i] + xP[ti]) : 0.f;                   // E
                 const float f = j < ti ? -dc * (xx[i] + xX[ti]) : 0.f;                   // F
                 xP[ti] = f;
                 kk[i] = j < ti ? f * kk[i] + x * qk[i] : 0.f;                            // M
@@ -574,6 +574,8 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_grad_tc_kernel(const __grid_c
 }  // namespace
 
 namespace bwd {
+
+cudaError_t set_wait_limit_tc(unsigned long long ns) { return set_module_wait_limit(ns); }
 
 cudaError_t launch_grad_tc(const BwdParams &p, cudaStream_t stream)
 {

@@ -134,6 +134,7 @@ cudaError_t device_error_word(int **ptr);
 // its own copy), on the current device.
 cudaError_t set_wait_limit_pool(unsigned long long ns);
 cudaError_t set_wait_limit_tc(unsigned long long ns);
+cudaError_t set_wait_limit_backward(unsigned long long ns);
 
 // Launch accounting (gdn_kernel_launches).
 void count_launches(int n);

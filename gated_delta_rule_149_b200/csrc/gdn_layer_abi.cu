@@ -2,6 +2,7 @@
 // gradients.  Every argument error is caught before anything is launched; no C++ exception crosses.
 #include <cuda_runtime.h>
 
+#include <climits>
 #include <cmath>
 #include <cstdint>
 
@@ -39,6 +40,7 @@ int check_sizes(int B, int H, int T, int d, int least, int step, const char *d_n
 {
     if (B <= 0 || H <= 0 || T <= 0)
         return fail(GDN_ERR_INVALID_ARG, "B, H and T must be positive (got %d, %d, %d)", B, H, T);
+    if (T > INT_MAX - 64) return fail(GDN_ERR_UNSUPPORTED, "T = %d is too long", T);
     if ((long long)B * H > 65535) return fail(GDN_ERR_UNSUPPORTED, "B*H = %lld exceeds 65535", (long long)B * H);
     if (d < least || d % step || d > 256)
         return fail(GDN_ERR_UNSUPPORTED, "%s must be a multiple of %d in [%d, 256] (got %d)", d_name, step, least, d);

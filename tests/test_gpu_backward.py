@@ -164,6 +164,61 @@ def test_own_stream_and_graphs():
         assert all(torch.equal(x, y) for x, y in zip(want, out))
 
 
+def test_two_streams_at_once():
+    """Two different calls in flight on two streams share no state."""
+    calls = [[None if x is None else x.cuda() for x in make(1, 4, 700, 128, 128, "bf16", seed, True, True, shift=2.0)] for seed in (51, 52)]
+    want = [gdn_backward(*c, bidi=True) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = []
+    for _ in range(3):
+        got = [gdn_backward(*c, bidi=True, stream=s) for c, s in zip(calls, streams)]
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        assert all(torch.equal(x, y) for x, y in zip(w, g))
+
+
+@pytest.mark.parametrize("T,heads", [(64 * 100, 230)])
+def test_heads_in_several_passes(T, heads):
+    """More heads and chunks than one pass's workspace holds (6 GiB): each head as in a call of its own.  The two calls may
+    take other forms of the chains, which add in another order: within fp32's rounding of one another (1e-5)."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    n = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+    q, k = (torch.nn.functional.normalize(n(1, heads, T, 128), dim=-1).bfloat16() for _ in range(2))
+    v, do = n(1, heads, T, 128).bfloat16(), n(1, heads, T, 128).bfloat16()
+    beta, decay = torch.sigmoid(n(1, heads, T)), torch.sigmoid(3 + n(1, heads, T))
+    s0, ds = 0.1 * n(1, heads, 128, 128), n(1, heads, 128, 128)
+    whole = gdn_backward(q, k, v, beta, decay, do, s0, ds)
+    for at in (0, heads // 2 - 1, heads // 2, heads - 1):
+        one = gdn_backward(*(x[:, at:at + 1].contiguous() for x in (q, k, v, beta, decay, do, s0, ds)))
+        for name, x, y in zip(NAMES, whole, one):
+            tol = 1e-5 + (2.0 ** -8 if x.dtype == torch.bfloat16 else 0.0)
+            assert ref.rel(x[:, at:at + 1].double(), y.double()) <= tol, (name, at)
+
+
+@pytest.mark.parametrize("dtype,dk", [("fp32", 64), ("bf16", 128)])
+def test_non_finite_values_stay_in_their_chunk(dtype, dk):
+    """A NaN in do at token 70: what the definition keeps apart from it stays finite outside tokens 64 .. 127, and another
+    head is untouched."""
+    a = make(1, 2, 200, dk, 64, dtype, 61, False, True)
+    clean = run(a, False)
+    a[5][0, 0, 70, 3] = float("nan")
+    got = run(a, False)
+    for name, x, y in zip(NAMES, got, clean):
+        assert torch.equal(x[0, 1], y[0, 1]), name
+        if name == "dq":
+            assert torch.equal(x[0, 0, :64], y[0, 0, :64]) and torch.equal(x[0, 0, 128:], y[0, 0, 128:])
+        elif name != "dstate_in":
+            assert torch.equal(x[0, 0, 128:], y[0, 0, 128:]), name
+
+
+def test_many_short_scans_and_one_long():
+    """The chains' two forms: more scans than SMs, and a few."""
+    check(make(3, 30, 20, 128, 128, "bf16", 71, True, True), True)
+    check(make(1, 1, 1500, 128, 64, "bf16", 72, False, True, shift=-2.0), False)
+    check(make(2, 40, 33, 64, 64, "fp32", 73, True, True), True)
+
+
 def test_refuses_what_it_does_not_take():
     a = [None if x is None else x.cuda() for x in make(1, 2, 10, 64, 64, "fp32", 1, False, True)]
     for i in range(8):

@@ -94,7 +94,7 @@ def test_backward_misaligned(lib, name):
 
 
 @pytest.mark.parametrize("kw,code", [(dict(T=0), -1), (dict(B=-1), -1), (dict(mode=8), -1), (dict(mode=16), -1), (dict(mode=4), -2),
-                                     (dict(dk=48), -2), (dict(dv=160), -2), (dict(B=256, H=256), -2)])
+                                     (dict(dk=48), -2), (dict(dv=160), -2), (dict(B=256, H=256), -2), (dict(T=2 ** 31 - 1), -2)])
 def test_backward_sizes_and_modes(lib, kw, code):
     assert bwd(lib, **kw) == code
 
@@ -116,7 +116,7 @@ def rot(lib, back=False, q=True, k=True, dq=True, dk=True, yq=True, yk=True, **k
     (dict(q=None), -1), (dict(yq=None), -1), (dict(yk=None), -1), (dict(k=None), -1), (dict(q=view(0)), -1),
     (dict(q=view(PM)), -3), (dict(yk=view(PM)), -3), (dict(q=view(sb=-1)), -1), (dict(q=view(st=1 << 62)), -1),
     (dict(yq=view(st=8)), -1), (dict(yq=view(sh=0)), -1),
-    (dict(B=0), -1), (dict(H=0), -1), (dict(T=0), -1), (dict(B=300, H=300), -2), (dict(d=31), -2), (dict(d=0, axes=(0, 0, 0)), -2),
+    (dict(B=0), -1), (dict(H=0), -1), (dict(T=0), -1), (dict(B=300, H=300), -2), (dict(T=2 ** 31 - 1), -2), (dict(d=31), -2), (dict(d=0, axes=(0, 0, 0)), -2),
     (dict(d=258, axes=(258, 0, 0)), -2), (dict(axes=(12, 10, 8)), -1), (dict(axes=(11, 11, 10)), -1), (dict(axes=(-2, 24, 10)), -1),
     (dict(gh=0), -1), (dict(gw=-1), -1), (dict(start=-1), -1), (dict(start=(1 << 52) + 1), -1), (dict(theta=0.0), -1),
     (dict(theta=float("nan")), -1), (dict(theta=float("inf")), -1), (dict(eps=0.0, mode=32), -1), (dict(eps=float("nan"), mode=32), -1),
