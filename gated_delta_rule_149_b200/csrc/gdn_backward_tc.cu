@@ -251,7 +251,7 @@ __device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint
             bwd::copy_tile(base + Smem::Q, unit + U1::Q, kKeys, kWorkers);
             bwd::copy_tile(base + Smem::O, p.ot + t.ws * p.slices * (64 * 64), p.slices * 64 * 64, kWorkers);
             bwd::copy_commit();
-            Step now, next;
+            Step now;
             auto fetch = [&](Step &x, int step) {
                 const size_t st = (size_t)step * kRows * 128, rw = (size_t)step * kRows * 64;
                 read4(HT + st, x.h);
@@ -268,7 +268,6 @@ __device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint
                     }
                 }
             };
-            fetch(next, 0);
             bwd::copy_wait<0>();
             named_bar(1, kWorkers);
 
@@ -276,8 +275,7 @@ __device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint
             for (int step = 0; step < steps; ++step) {
                 const int b = step & 1;
                 unsigned char *const at = sm + Smem::buf + b * kBuf;
-                now = next;
-                if (step + 1 < steps) fetch(next, step + 1);
+                fetch(now, step);
                 if (step >= 2) {
                     ok = ok && wait_bar(&s.done[b], phase[b], &s.abort, p.err, 64);
                     phase[b] ^= 1;
