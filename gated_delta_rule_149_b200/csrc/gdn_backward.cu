@@ -60,6 +60,8 @@ struct PrepSmem {
     struct Solve {
         float X[kC * (kC + 4)];    // X diag(b)
         float N[kC * (kC + 4)];
+        float inv[4 * 16 * 20];    // the inverses of the 16 x 16 diagonal blocks of I + X diag(b)
+        float rows[16 * (kC + 4)];
     };
     union {                        // K and Q are done with when X is there: small blocks, four to an SM
         Keys k;
@@ -99,7 +101,7 @@ __device__ __forceinline__ void get8(const T *row, bool on, int c, int len, floa
     for (int i = 0; i < 8; ++i) x[i] = 0.f;
     if (!on || c >= len) return;
     if constexpr (sizeof(T) == 2) {
-        const uint4 u = *reinterpret_cast<const uint4 *>(row + c);
+        const uint4 u = __ldg(reinterpret_cast<const uint4 *>(row + c));
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -107,7 +109,7 @@ __device__ __forceinline__ void get8(const T *row, bool on, int c, int len, floa
             x[2 * i + 1] = hi16(w[i]);
         }
     } else {
-        const float4 u = reinterpret_cast<const float4 *>(row + c)[0], v = reinterpret_cast<const float4 *>(row + c)[1];
+        const float4 u = __ldg(reinterpret_cast<const float4 *>(row + c)), v = __ldg(reinterpret_cast<const float4 *>(row + c) + 1);
         x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
         x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
     }
@@ -157,32 +159,66 @@ __global__ void __launch_bounds__(kPrepThreads, NI == 1 ? 4 : 1) bwd_prepare_ker
     }
     const T *kb = static_cast<const T *>(p.k) + (size_t)t.head * p.T * p.dk;
     const T *qb = static_cast<const T *>(p.q) + (size_t)t.head * p.T * p.dk;
-    for (int e = tid; e < kC * (DK / 8); e += kPrepThreads) {
-        const int i = e / (DK / 8), c = e % (DK / 8);
-        const bool on = i < t.n;
-        const size_t row = on ? (size_t)t.tok(i) * p.dk : 0;
-        float x[8];
-        get8(kb + row, on, 8 * c, p.dk, x);
-        put8<NI, kKeyRow<DK>, T>(x, i, c, s.k.K, unit + U::K, U::kKey);
-        get8(qb + row, on, 8 * c, p.dk, x);
-        put8<NI, kKeyRow<DK>, T>(x, i, c, s.k.Q, unit + U::Q, U::kKey);
-    }
     const T *vb = static_cast<const T *>(p.v) + (size_t)t.head * p.T * p.dv;
     const T *ob = static_cast<const T *>(p.dout) + (size_t)t.head * p.T * p.dv;
-    for (int e = tid; e < p.slices * kC * 4; e += kPrepThreads) {
-        const int sl = e / (kC * 4), i = e / 4 % kC, c = e % 4;
-        const bool on = i < t.n;
-        const size_t row = on ? (size_t)t.tok(i) * p.dv : 0;
-        float x[8];
-        get8(ob + row, on, sl * kSlice + 8 * c, p.dv, x);
-        put8<NI, 64, T>(x, i, c, nullptr, p.ot + (t.ws * p.slices + sl) * (NI * kC * 64), kC * 64);
-        get8(vb + row, on, sl * kSlice + 8 * c, p.dv, x);
-        unsigned char *vt = p.vt + (t.ws * p.slices + sl) * (kC * kSlice * sizeof(T));
-        if constexpr (sizeof(T) == 2) {
-            put8<1, 64, T>(x, i, c, nullptr, vt, 0);
-        } else {
-            *reinterpret_cast<float4 *>(vt + sw<128>(i, 2 * c)) = make_float4(x[0], x[1], x[2], x[3]);
-            *reinterpret_cast<float4 *>(vt + sw<128>(i, 2 * c + 1)) = make_float4(x[4], x[5], x[6], x[7]);
+    unsigned char *const ot = p.ot + t.ws * p.slices * (NI * kC * 64), *const vt = p.vt + t.ws * p.slices * (kC * kSlice * sizeof(T));
+    if constexpr (NI == 1) {
+        // bf16 is its own term: the pieces move as they are, all loads of a tensor pair in flight together
+        auto piece = [&](const T *x, int len, int i, int c) {
+            return i < t.n && c < len ? __ldg(reinterpret_cast<const uint4 *>(x + (size_t)t.tok(i) * len + c)) : make_uint4(0, 0, 0, 0);
+        };
+        constexpr int IT = kC * DK / 8 / kPrepThreads;
+        uint4 x[4], y[4];
+#pragma unroll
+        for (int u = 0; u < IT; ++u) {
+            const int e = tid + u * kPrepThreads, i = e / (DK / 8), c = e % (DK / 8);
+            x[u] = piece(kb, p.dk, i, 8 * c);
+            y[u] = piece(qb, p.dk, i, 8 * c);
+        }
+#pragma unroll
+        for (int u = 0; u < IT; ++u) {
+            const int e = tid + u * kPrepThreads;
+            const uint32_t o = sw<kKeyRow<DK>>(e / (DK / 8), e % (DK / 8));
+            *reinterpret_cast<uint4 *>(s.k.K + o) = x[u];
+            *reinterpret_cast<uint4 *>(s.k.Q + o) = y[u];
+            *reinterpret_cast<uint4 *>(unit + U::K + o) = x[u];
+            *reinterpret_cast<uint4 *>(unit + U::Q + o) = y[u];
+        }
+        const int i = tid >> 2, c = tid & 3;
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (u < p.slices) {
+                x[u] = piece(ob, p.dv, i, u * kSlice + 8 * c);
+                y[u] = piece(vb, p.dv, i, u * kSlice + 8 * c);
+            }
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (u < p.slices) {
+                *reinterpret_cast<uint4 *>(ot + u * (kC * 64) + sw<64>(i, c)) = x[u];
+                *reinterpret_cast<uint4 *>(vt + u * (kC * 64) + sw<64>(i, c)) = y[u];
+            }
+    } else {
+        for (int e = tid; e < kC * (DK / 8); e += kPrepThreads) {
+            const int i = e / (DK / 8), c = e % (DK / 8);
+            const bool on = i < t.n;
+            const size_t row = on ? (size_t)t.tok(i) * p.dk : 0;
+            float x[8], y[8];
+            get8(kb + row, on, 8 * c, p.dk, x);
+            get8(qb + row, on, 8 * c, p.dk, y);
+            put8<NI, kKeyRow<DK>, T>(x, i, c, s.k.K, unit + U::K, U::kKey);
+            put8<NI, kKeyRow<DK>, T>(y, i, c, s.k.Q, unit + U::Q, U::kKey);
+        }
+        for (int e = tid; e < p.slices * kC * 4; e += kPrepThreads) {
+            const int sl = e / (kC * 4), i = e / 4 % kC, c = e % 4;
+            const bool on = i < t.n;
+            const size_t row = on ? (size_t)t.tok(i) * p.dv : 0;
+            float x[8], y[8];
+            get8(ob + row, on, sl * kSlice + 8 * c, p.dv, x);
+            get8(vb + row, on, sl * kSlice + 8 * c, p.dv, y);
+            put8<NI, 64, T>(x, i, c, nullptr, ot + sl * (NI * kC * 64), kC * 64);
+            unsigned char *to = vt + sl * (kC * kSlice * sizeof(T));
+            *reinterpret_cast<float4 *>(to + sw<128>(i, 2 * c)) = make_float4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<float4 *>(to + sw<128>(i, 2 * c + 1)) = make_float4(y[4], y[5], y[6], y[7]);
         }
     }
     __syncthreads();
@@ -234,38 +270,51 @@ __global__ void __launch_bounds__(kPrepThreads, NI == 1 ? 4 : 1) bwd_prepare_ker
                 *reinterpret_cast<uint32_t *>(unit + U::P + x3 * kTri + sw<128>(i, j >> 3) + (j & 7) * 2) = u[x3];
         }
     __syncthreads();
-    // N <- X - (X diag(b)) N in block rows of 16: the rows above by all threads, the 16 x 16 triangle by one
-    // thread per column
+    // N = (I + L)^-1 X, L = X diag(b), in block rows of 16: the inverses of the diagonal blocks first, all four at once by
+    // a thread per column; then each block row, N_I = (I + L_II)^-1 (X_I - L_I N), by all threads
+    if (tid < kC) {
+        const int r = 16 * (tid >> 4), c = tid & 15;
+        float y[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            y[i] = i == c ? 1.f : 0.f;
+#pragma unroll
+            for (int l = 0; l < i; ++l) y[i] = fmaf(-s.n.X[(r + i) * ld + r + l], y[l], y[i]);
+            s.n.inv[((tid >> 4) * 16 + i) * 20 + c] = y[i];
+        }
+    }
     for (int r = 0; r < kC; r += 16) {
-        if (r) {
-            const int i = r + (tid >> 4), j = 4 * (tid & 15);
-            float4 y = *reinterpret_cast<float4 *>(&s.n.N[i * ld + j]);
-            for (int l = 0; l < r; l += 4) {
-                const float4 x = *reinterpret_cast<const float4 *>(&s.n.X[i * ld + l]);
-                const float xs[4] = {x.x, x.y, x.z, x.w};
+        const int i = tid >> 4, j = 4 * (tid & 15);
+        float4 y = *reinterpret_cast<float4 *>(&s.n.N[(r + i) * ld + j]);
+        for (int l = 0; l < r; l += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(&s.n.X[(r + i) * ld + l]);
+            const float xs[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const float4 n = *reinterpret_cast<const float4 *>(&s.n.N[(l + u) * ld + j]);
-                    y.x = fmaf(-xs[u], n.x, y.x);
-                    y.y = fmaf(-xs[u], n.y, y.y);
-                    y.z = fmaf(-xs[u], n.z, y.z);
-                    y.w = fmaf(-xs[u], n.w, y.w);
-                }
-            }
-            *reinterpret_cast<float4 *>(&s.n.N[i * ld + j]) = y;
-            __syncthreads();
-        }
-        if (tid < kC) {
-            const int j = tid;
-            float y[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                y[i] = s.n.N[(r + i) * ld + j];
-#pragma unroll
-                for (int l = 0; l < i; ++l) y[i] = fmaf(-s.n.X[(r + i) * ld + r + l], y[l], y[i]);
-                s.n.N[(r + i) * ld + j] = y[i];
+            for (int u = 0; u < 4; ++u) {
+                const float4 n = *reinterpret_cast<const float4 *>(&s.n.N[(l + u) * ld + j]);
+                y.x = fmaf(-xs[u], n.x, y.x);
+                y.y = fmaf(-xs[u], n.y, y.y);
+                y.z = fmaf(-xs[u], n.z, y.z);
+                y.w = fmaf(-xs[u], n.w, y.w);
             }
         }
+        *reinterpret_cast<float4 *>(&s.n.rows[i * ld + j]) = y;
+        __syncthreads();
+        y = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int l = 0; l < 16; l += 4) {
+            const float4 x = *reinterpret_cast<const float4 *>(&s.n.inv[(r + i) * 20 + l]);
+            const float xs[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float4 n = *reinterpret_cast<const float4 *>(&s.n.rows[(l + u) * ld + j]);
+                y.x = fmaf(xs[u], n.x, y.x);
+                y.y = fmaf(xs[u], n.y, y.y);
+                y.z = fmaf(xs[u], n.z, y.z);
+                y.w = fmaf(xs[u], n.w, y.w);
+            }
+        }
+        *reinterpret_cast<float4 *>(&s.n.N[(r + i) * ld + j]) = y;
         __syncthreads();
     }
     for (int e = tid; e < kC * kC / 8; e += kPrepThreads) {
@@ -280,8 +329,9 @@ __global__ void __launch_bounds__(kPrepThreads, NI == 1 ? 4 : 1) bwd_prepare_ker
 // ---------------------------------------------------------------- chains
 // Grid (groups of 16 PAIRS columns of dv, heads, directions and walks).  A pair of warps carries 16 columns: each holds
 // half of dk of H^T; their partial H^T K^T meet in shared memory, and again their halves of the triangular product, and
-// both go on with the whole of W (or Z).  One warp per 16 columns would spare that, but takes
-// 8.9 us for a chunk of 64 tokens (dk = dv = 128, bf16): a walk is bound by its own latency, and the pair shortens it.
+// both go on with the whole of W (or Z).  One warp per 16 columns would spare the exchanges, but takes 8.9 us for a
+// chunk of 64 tokens (dk = dv = 128, bf16, one warp to a scheduler) where the pairs take 6.2 with two: a walk is bound by
+// its own dependent steps.  The products are at 62 % of what mma.sync reaches here (970 multiply-adds a cycle and SM).
 
 // A stage's two bulk copies, issued by one thread (sixteen-byte copies by all threads took 1000 of a chunk's 7300 cycles)
 // and awaited by all.
@@ -575,7 +625,7 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
 // counts.  A warp holds a quarter of dk of H^T.  Its partial H^T K^T goes to the others by tokens: warp q adds up tokens
 // 16 q .. 16 q + 15, multiplies them into its part of the triangular product, whose sums by tokens meet the same way,
 // and shares the finished W (or Z) of its tokens as left operands; nothing but the shared operands' loads is done twice.
-// (480p chunk, 16 heads of 74 chunks, dk = dv = 128, bf16: 4.7 us a chunk with pairs of warps.)
+// (480p chunk, 16 heads of 74 chunks, dk = dv = 128, bf16: 3.7 us a chunk, 4.7 with pairs of warps.)
 template <int DK, int NI, typename T, int WALK>
 struct StageNarrow {
     using U = Unit<DK, NI>;
