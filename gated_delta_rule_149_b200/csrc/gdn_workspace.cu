@@ -39,18 +39,23 @@ cudaError_t pool_of(int dev, bool create, cudaMemPool_t *out)
         props.location.type = cudaMemLocationTypeDevice;
         props.location.id = dev;
         cudaMemPool_t p = nullptr;
-        cudaError_t err = cudaMemPoolCreate(&p, &props);
+        // a first call may come inside a stream capture, which by default forbids calls like these
+        cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+        cudaError_t err = cudaThreadExchangeStreamCaptureMode(&mode);
         if (err != cudaSuccess) return err;
+        err = cudaMemPoolCreate(&p, &props);
         uint64_t keep = UINT64_MAX;
-        err = cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
+        if (err == cudaSuccess) err = cudaMemPoolSetAttribute(p, cudaMemPoolAttrReleaseThreshold, &keep);
         // A block freed on one stream is not handed to an allocation on another
         // by making that stream wait (calls on two streams stay concurrent); it
         // is reused once its free has completed, or through existing event order.
         int no_hidden_waits = 0;
         if (err == cudaSuccess)
             err = cudaMemPoolSetAttribute(p, cudaMemPoolReuseAllowInternalDependencies, &no_hidden_waits);
+        const cudaError_t back = cudaThreadExchangeStreamCaptureMode(&mode);
+        if (err == cudaSuccess) err = back;
         if (err != cudaSuccess) {
-            cudaMemPoolDestroy(p);
+            if (p) cudaMemPoolDestroy(p);
             return err;
         }
         g_pool[dev] = p;

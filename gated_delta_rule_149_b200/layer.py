@@ -176,7 +176,8 @@ def gdn_gated_norm(o, gate=None, weight=None, *, eps=1e-5, stream=None):
 
 def gdn_gated_norm_backward(dy, o, gate=None, weight=None, *, eps=1e-5, stream=None):
     """Gradients of gdn_gated_norm from dy [B,T,H*dv]: do (contiguous [B,H,T,dv], as gdn_backward takes it), dgate
-    ([B,H,T,dv] in [B,T,H,dv] memory; None without gate) and dweight (fp32, shape of weight; None without)."""
+    ([B,H,T,dv] in [B,T,H,dv] memory; None without gate) and dweight (fp32, shape of weight; None without).  An
+    expanded input's gradient comes per element, like any other's."""
     shape = _shape(o, "o")
     B, H, T, dv = shape
     dev, lib = o.device, load_library()

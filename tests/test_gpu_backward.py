@@ -2,6 +2,10 @@
 
 Tolerances (rel-L2): fp32 outputs 1e-5, the library's bar for fp32 arithmetic; outputs of bf16 type half a step of
 the type on every value, 2^-8, and that."""
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -162,6 +166,30 @@ def test_own_stream_and_graphs():
     torch.cuda.synchronize()
     for _, out in graphs:
         assert all(torch.equal(x, y) for x, y in zip(want, out))
+
+
+FIRST_IN_CAPTURE = """
+import torch
+from gated_delta_rule_149_b200 import gdn_backward
+x = [torch.randn(1, 2, 100, 128, device="cuda").bfloat16() for _ in range(4)]
+g = [torch.rand(1, 2, 100, device="cuda") for _ in range(2)]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = gdn_backward(0.1 * x[0], 0.1 * x[1], x[2], *g, x[3])
+graph.replay()
+want = gdn_backward(0.1 * x[0], 0.1 * x[1], x[2], *g, x[3])
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) for a, b in zip(out, want))
+print("same")
+"""
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    """The library's pool of device memory comes into being on first use, which may be within a capture."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], cwd=root, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]
 
 
 def test_two_streams_at_once():
