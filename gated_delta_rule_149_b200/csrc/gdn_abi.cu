@@ -196,7 +196,7 @@ int host_call(const void *q, const void *k, const void *v, const float *beta, co
 
 extern "C" {
 
-int gdn_version(void) { return 10000; }
+int gdn_version(void) { return 10100; }
 
 const char *gdn_last_error(void) { return g_msg; }
 
