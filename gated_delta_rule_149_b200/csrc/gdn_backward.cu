@@ -26,17 +26,17 @@
 // Products run on the tensor cores with bf16 operands and fp32 sums, at fp32 grade: an fp32 operand is three bf16
 // terms, x = h + m + l (24 bits of significand), and of the products of terms those of total order under three are
 // taken; a bf16 input is one term and exact.  Two terms would halve the products and leave 3e-6 (rel-L2) in the fp32
-// gradients where three leave 2e-7; only dQ's and dK's products with E and F, whose results are rounded to
-// bf16, take two.
+// gradients where three leave 2e-7; only the products with E and F, where their results (dQ, dK) are rounded to bf16,
+// take two.
 //
 // Kernels:
 // * prepare (a block per chunk and direction): brings K, Q, V, dO into scan order as term planes in the
 //   layout that the other two load without conversion, forms N and P likewise.
 // * chains (two serial walks, forward for H0 and W, backward for dH1 and Z, which need nothing of one another
-//   and run side by side): the columns of dv are independent, and a warp carries 16 of them through the whole
-//   sequence by itself.  It holds H^T (16 x dk) as accumulator fragments, which are, split into terms, the left
-//   operands of the next product; so the walk's three dependent products pass through registers, no state goes through
-//   shared memory, and the block's barrier only paces the double-buffered operands.
+//   and run side by side): the columns of dv are independent, and two or four warps carry 16 of them through the
+//   whole sequence.  They hold H^T (16 x dk) as accumulator fragments, which are, split into terms, the left
+//   operands of the next product; so no state goes through shared memory, only sums over dk and over tokens meet
+//   there, and the block's barrier paces the double-buffered operands.
 // * gradients (a block per chunk, both scan directions, so that a bidirectional call's sums are rounded once).
 #include <algorithm>
 #include <cstdint>

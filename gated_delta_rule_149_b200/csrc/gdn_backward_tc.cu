@@ -11,9 +11,9 @@
 // shared memory, as operands with the contraction's index as their row (MN-major), in two buffers, so that the next
 // step's loads and splitting run beside the tensor core.  One warp issues the products: a product of 128 x 64 x 16 takes
 // the tensor core 48 cycles, its issue as long, and a step has 42 of them, which the splitting must not wait for.  (1184
-// chunks, dv = 128: 170 us, where mma.sync tiles took 280; the tensor core is busy for a quarter of that, the rest is the
-// latency of loads, splitting and epilogue with sixteen warps of 96 registers.)  Products of terms are those of order i + j < 3, the small
-// ones first.
+// chunks, dv = 128: 170 us, where mma.sync tiles took 280; the tensor core is busy for a third of that, the rest is the
+// latency of loads, splitting and epilogue with sixteen warps of 96 registers.)  Products of terms are those of order
+// i + j < 3, the small ones first.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
