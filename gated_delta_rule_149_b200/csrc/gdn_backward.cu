@@ -126,37 +126,39 @@ __global__ void __launch_bounds__(kPrepThreads, NI == 1 ? 4 : 1) bwd_prepare_ker
     unsigned char *unit = p.unit + t.ws * U::size;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
-    if (warp == 0) {
-        double l[2];
+    auto gates = [&] {
+        if (warp == 0) {
+            double l[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int i = 2 * lane + h;
-            float a = 1.f, b = 0.f;
-            if (i < t.n) {
-                const size_t at = (size_t)t.head * p.T + t.tok(i);
-                a = fmaxf(p.decay[at], 7.52316385e-37f);   // 2^-120
-                b = p.beta[at];
+            for (int h = 0; h < 2; ++h) {
+                const int i = 2 * lane + h;
+                float a = 1.f, b = 0.f;
+                if (i < t.n) {
+                    const size_t at = (size_t)t.head * p.T + t.tok(i);
+                    a = fmaxf(p.decay[at], 7.52316385e-37f);   // 2^-120
+                    b = p.beta[at];
+                }
+                s.g.a[i] = a;
+                s.g.b[i] = b;
+                l[h] = (double)log2f(a);
             }
-            s.g.a[i] = a;
-            s.g.b[i] = b;
-            l[h] = (double)log2f(a);
-        }
-        double sum = l[0] + l[1];
+            double sum = l[0] + l[1];
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const double y = __shfl_up_sync(0xffffffffu, sum, o);
-            if (lane >= o) sum += y;
+            for (int o = 1; o < 32; o <<= 1) {
+                const double y = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += y;
+            }
+            const double end = __shfl_sync(0xffffffffu, sum, 31), first = sum - l[1];
+            s.g.high[2 * lane] = (float)first;
+            s.g.low[2 * lane] = (float)(first - (double)(float)first);
+            s.g.high[2 * lane + 1] = (float)sum;
+            s.g.low[2 * lane + 1] = (float)(sum - (double)(float)sum);
+            s.g.gam[2 * lane] = exp2f((float)first);
+            s.g.gam[2 * lane + 1] = exp2f((float)sum);
+            s.g.e[2 * lane] = exp2f((float)(end - first));
+            s.g.e[2 * lane + 1] = exp2f((float)(end - sum));
         }
-        const double end = __shfl_sync(0xffffffffu, sum, 31), first = sum - l[1];
-        s.g.high[2 * lane] = (float)first;
-        s.g.low[2 * lane] = (float)(first - (double)(float)first);
-        s.g.high[2 * lane + 1] = (float)sum;
-        s.g.low[2 * lane + 1] = (float)(sum - (double)(float)sum);
-        s.g.gam[2 * lane] = exp2f((float)first);
-        s.g.gam[2 * lane + 1] = exp2f((float)sum);
-        s.g.e[2 * lane] = exp2f((float)(end - first));
-        s.g.e[2 * lane + 1] = exp2f((float)(end - sum));
-    }
+    };
     const T *kb = static_cast<const T *>(p.k) + (size_t)t.head * p.T * p.dk;
     const T *qb = static_cast<const T *>(p.q) + (size_t)t.head * p.T * p.dk;
     const T *vb = static_cast<const T *>(p.v) + (size_t)t.head * p.T * p.dv;
@@ -175,6 +177,7 @@ __global__ void __launch_bounds__(kPrepThreads, NI == 1 ? 4 : 1) bwd_prepare_ker
             x[u] = piece(kb, p.dk, i, 8 * c);
             y[u] = piece(qb, p.dk, i, 8 * c);
         }
+        gates();                                               // beside the loads
 #pragma unroll
         for (int u = 0; u < IT; ++u) {
             const int e = tid + u * kPrepThreads;
@@ -198,6 +201,7 @@ __global__ void __launch_bounds__(kPrepThreads, NI == 1 ? 4 : 1) bwd_prepare_ker
                 *reinterpret_cast<uint4 *>(vt + u * (kC * 64) + sw<64>(i, c)) = y[u];
             }
     } else {
+        gates();
         for (int e = tid; e < kC * (DK / 8); e += kPrepThreads) {
             const int i = e / (DK / 8), c = e % (DK / 8);
             const bool on = i < t.n;
