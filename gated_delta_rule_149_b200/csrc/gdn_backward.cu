@@ -135,7 +135,8 @@ __global__ void __launch_bounds__(kPrepThreads, NI == 1 ? 4 : 1) bwd_prepare_ker
                 float a = 1.f, b = 0.f;
                 if (i < t.n) {
                     const size_t at = (size_t)t.head * p.T + t.tok(i);
-                    a = fmaxf(p.decay[at], 7.52316385e-37f);   // 2^-120
+                    a = p.decay[at];
+                    a = a < 7.52316385e-37f ? 7.52316385e-37f : a;   // 2^-120; a NaN stays one
                     b = p.beta[at];
                 }
                 s.g.a[i] = a;

@@ -299,7 +299,8 @@ int gdn_forward_fp8(const void *q8, const void *k8, const void *v8,
  *
  * dk, dv: multiples of 32, <= 128, for both dtypes.  beta may be 0.  A decay below
  * 2^-120 acts as 2^-120 and has the gradient of that value.  A non-finite value
- * spreads over the 64-token chunk that holds it, and further as the formula has it.
+ * (a decay that is NaN among them) spreads over the 64-token chunk that holds it,
+ * and further as the formula has it.
  * Same results on every call with the same arguments (no atomics).  Workspace
  * (stream-ordered) per head, 64-token chunk and direction: 8 dk dv + 256 dk + 768 dv
  * + 50,688 bytes in bf16, 8 dk dv + 768 dk + 1152 dv + 50,688 in fp32, dk rounded up
