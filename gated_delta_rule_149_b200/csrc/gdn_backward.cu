@@ -1107,6 +1107,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
             }
         }
         __syncthreads();               // the walk's planes are done with: E, F, M take their place
+        const Lift lift = lift_of(s.g);
 #pragma unroll
         for (int n = 0; n < 4; ++n)
 #pragma unroll
@@ -1115,11 +1116,12 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
                 float x[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float d = j + c <= i ? s.g.decay(i, j + c) : 0.f;
+                    const float d = j + c <= i ? s.g.decay(i, j + c, lift.shift) : 0.f;
                     const float f = j + c < i ? -d * dx[n][2 * h + c] : 0.f;
                     x[c] = j + c <= i ? d * dp[n][2 * h + c] : 0.f;
-                    s.tail.F[i * kLdT + j + c] = f;
+                    s.tail.F[i * kLdT + j + c] = f * lift.down;
                     s.tail.M[i * (kC + 1) + j + c] = j + c < i ? f * kk[n][2 * h + c] + x[c] * qk[n][2 * h + c] : 0.f;
+                    x[c] *= lift.down;
                 }
                 uint32_t u[NE];
                 split2<NE>(x[0], x[1], u);
@@ -1150,8 +1152,8 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
             y += __shfl_xor_sync(0xffffffffu, y, 1);
             y += __shfl_xor_sync(0xffffffffu, y, 2);
             if ((lane & 3) == 0) {
-                s.m0[wn][i] = gam * x;
-                s.m1[wn][i] = e * y;
+                s.m0[wn][i] = s.g.from_entry(i, lift.shift) * x;
+                s.m1[wn][i] = s.g.decay(kC - 1, i, lift.shift) * y;
             }
         }
         __syncthreads();
@@ -1178,7 +1180,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
                 from = 0.f;
 #pragma unroll
                 for (int w = 0; w < 8; ++w) from += s.hh[w];
-                from *= s.g.gam[kC - 1];
+                from *= s.g.from_entry(kC - 1, lift.shift);
             }
             float sum = x + y;
 #pragma unroll
@@ -1202,7 +1204,7 @@ __global__ void __launch_bounds__(kGradThreads, 1) bwd_grad_kernel(const __grid_
                 b += s.dbw[w][tid];
             }
             const int at = t.tok(tid) - t.c * kC;
-            s.da[at] += a / s.g.a[tid];
+            s.da[at] += a / (s.g.a[tid] * lift.up);
             s.db[at] += b;
         }
         // dQ = gam hdo + E K;  dK = e du - gam hy + S K + E^T Q

@@ -31,9 +31,28 @@ __device__ __forceinline__ void st2(__nv_bfloat16 *p, float x, float y)
 // leave differences of neighbours 1e-5 off.
 struct Gates {
     float gam[kC], e[kC], b[kC], a[kC], high[kC], low[kC];
-    // D_ij = 2^(G_i - G_j) for j <= i
-    __device__ __forceinline__ float decay(int i, int j) const { return exp2f((high[i] - high[j]) + (low[i] - low[j])); }
+    // 2^shift D_ij = 2^(G_i - G_j + shift) for j <= i, and 2^shift gam_i
+    __device__ __forceinline__ float decay(int i, int j, float shift = 0.f) const
+    {
+        return exp2f(((high[i] - high[j]) + shift) + (low[i] - low[j]));
+    }
+    __device__ __forceinline__ float from_entry(int i, float shift) const { return exp2f((high[i] + shift) + low[i]); }
 };
+
+// The products that a decay's gradient sums up (M) are the size of the decay, down to 2^-120 of the gradients given, and
+// would leave fp32's range before the division by it.  A chunk with a decay under 2^-40 holds them 2^60 times larger (an
+// exact factor): 24 bits then down to given gradients of 2^-42 at a decay of 2^-120, and of 2^-62 where none is under
+// 2^-40, without bringing products of ordinary decays, up to 2^67, out of range at the other end.
+struct Lift {
+    float shift, up, down;
+};
+// by whole warps
+__device__ __forceinline__ Lift lift_of(const Gates &g)
+{
+    const int lane = threadIdx.x & 31;
+    const bool strong = __any_sync(0xffffffffu, fminf(g.a[lane], g.a[lane + 32]) < 0x1p-40f);
+    return strong ? Lift{60.f, 0x1p60f, 0x1p-60f} : Lift{0.f, 1.f, 1.f};
+}
 
 // Workspace of one (direction, head, chunk), in bytes.  Tiles are row-major with the 16-byte pieces of a
 // row XOR-ed by the row's number, so that eight rows' pieces of one column lie in eight bank groups.

@@ -332,6 +332,7 @@ __device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint
                 db[i] += __shfl_xor_sync(0xffffffffu, db[i], 16);
                 if (lane < 16) dbw[warp * 64 + 4 * lane + i] = db[i];
             }
+            const bwd::Lift lift = bwd::lift_of(s.g);
             // m0_i = gam_i (q_i . H0 dO_i - k_i . H0 Y_i), m1_i = e_i k_i . dH1 U_i over this quadrant's dk
             const int d = 32 * quad + lane;                     // dk
             {
@@ -351,8 +352,8 @@ __device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint
                 }
                 const float m0 = sum_across(a), m1 = sum_across(b);
                 if (lane < 16) {
-                    s.m0[quad][t0 + lane] = s.g.gam[t0 + lane] * m0;
-                    s.m1[quad][t0 + lane] = s.g.e[t0 + lane] * m1;
+                    s.m0[quad][t0 + lane] = s.g.from_entry(t0 + lane, lift.shift) * m0;
+                    s.m1[quad][t0 + lane] = s.g.decay(63, t0 + lane, lift.shift) * m1;
                 }
             }
             // PP and XX stand as two parts, in lanes j and 64 + j: the two threads take eight tokens each, give the
@@ -395,12 +396,12 @@ __device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint
                     kk[i] = xK[(8 * group + i) ^ lane];
                     qk[i] = xQ[(8 * group + i) ^ lane];
                 }
-                const float dc = j <= ti ? s.g.decay(ti, j) : 0.f;
+                const float dc = j <= ti ? s.g.decay(ti, j, lift.shift) : 0.f;
                 const float x = j <= ti ? dc * (pp[i] + xP[ti]) : 0.f;                   // E
                 const float f = j < ti ? -dc * (xx[i] + xX[ti]) : 0.f;                   // F
-                xP[ti] = f;
+                xP[ti] = f * lift.down;
                 kk[i] = j < ti ? f * kk[i] + x * qk[i] : 0.f;                            // M
-                pp[i] = x;
+                pp[i] = x * lift.down;
             }
             {
                 uint32_t v[4][2];
@@ -462,10 +463,10 @@ __device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint
                     end += s.hh[i];
                     b += dbw[i * 64 + ti];
                 }
-                x += fmaf(end, s.g.gam[63], s.col[0][ti] + s.col[1][ti]);
+                x += fmaf(end, s.g.from_entry(63, lift.shift), s.col[0][ti] + s.col[1][ti]);
                 if (lane < 16 && ti < t.n) {
                     const int tok = t.tok(ti) - t.c * 64;
-                    s.da[tok] += x / s.g.a[ti];
+                    s.da[tok] += x / (s.g.a[ti] * lift.up);
                     s.db[tok] += b;
                 }
             }

@@ -298,7 +298,8 @@ int gdn_forward_fp8(const void *q8, const void *k8, const void *v8,
  * precision of the forward kernel that ran.
  *
  * dk, dv: multiples of 32, <= 128, for both dtypes.  beta may be 0.  A decay below
- * 2^-120 acts as 2^-120 and has the gradient of that value.  A non-finite value
+ * 2^-120 acts as 2^-120 and has the gradient of that value (full precision for
+ * gradients dout, dstate_out down to about 2^-40).  A non-finite value
  * (a decay that is NaN among them) spreads over the 64-token chunk that holds it,
  * and further as the formula has it.
  * Same results on every call with the same arguments (no atomics).  Workspace
