@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(kPrepThreads, NI == 1 ? 4 : 1) bwd_prepare_ker
                 }
                 s.g.a[i] = a;
                 s.g.b[i] = b;
-                l[h] = (double)log2f(a);
+                l[h] = log2_of(a);
             }
             double sum = l[0] + l[1];
 #pragma unroll
@@ -149,15 +149,19 @@ __global__ void __launch_bounds__(kPrepThreads, NI == 1 ? 4 : 1) bwd_prepare_ker
                 const double y = __shfl_up_sync(0xffffffffu, sum, o);
                 if (lane >= o) sum += y;
             }
-            const double end = __shfl_sync(0xffffffffu, sum, 31), first = sum - l[1];
-            s.g.high[2 * lane] = (float)first;
-            s.g.low[2 * lane] = (float)(first - (double)(float)first);
-            s.g.high[2 * lane + 1] = (float)sum;
-            s.g.low[2 * lane + 1] = (float)(sum - (double)(float)sum);
-            s.g.gam[2 * lane] = exp2f((float)first);
-            s.g.gam[2 * lane + 1] = exp2f((float)sum);
-            s.g.e[2 * lane] = exp2f((float)(end - first));
-            s.g.e[2 * lane + 1] = exp2f((float)(end - sum));
+            const double end = __shfl_sync(0xffffffffu, sum, 31), G[2] = {sum - l[1], sum};
+            const double end_whole = rint(end);
+            const float end_frac = (float)(end - end_whole);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const double whole = rint(G[h]);
+                const int n = (int)whole;
+                const float f = (float)(G[h] - whole);
+                s.g.whole[2 * lane + h] = n;
+                s.g.frac[2 * lane + h] = f;
+                s.g.gam[2 * lane + h] = power2(n, f);
+                s.g.e[2 * lane + h] = power2((int)end_whole - n, end_frac - f);
+            }
         }
     };
     const T *kb = static_cast<const T *>(p.k) + (size_t)t.head * p.T * p.dk;

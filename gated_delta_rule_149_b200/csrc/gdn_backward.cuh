@@ -26,32 +26,57 @@ __device__ __forceinline__ void st2(__nv_bfloat16 *p, float x, float y)
 }
 
 // Gates of a chunk in scan order, as prepare leaves them for the other kernels.  a is clamped as in the
-// forward kernels; behind the sequence's end a = 1 and b = 0.  The running sums of log2 a are formed in 64 bits and
-// held as two floats, high + low: a strong decay brings them to several hundred within a chunk, where one float would
-// leave differences of neighbours 1e-5 off.
+// forward kernels; behind the sequence's end a = 1 and b = 0.  The running sums G of log2 a are formed in 64 bits and
+// held as a whole number and a fraction in [-1/2, 1/2]: a strong decay brings them to several hundred within a chunk,
+// where one float would leave 2^G 1e-5 off.  2^(G_i - G_j) adds 2^-22 to what the logarithms
+// are off, and is 0 under 2^-126.
+
+// 2^(n + f), |f| <= 1
+__device__ __forceinline__ float power2(int n, float f)
+{
+    float x;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(x) : "f"(f));
+    return x * __int_as_float((min(max(n, -127), 128) + 127) << 23);
+}
+
 struct Gates {
-    float gam[kC], e[kC], b[kC], a[kC], high[kC], low[kC];
+    float gam[kC], e[kC], b[kC], a[kC];
+    int whole[kC];
+    float frac[kC];
     // 2^shift D_ij = 2^(G_i - G_j + shift) for j <= i, and 2^shift gam_i
-    __device__ __forceinline__ float decay(int i, int j, float shift = 0.f) const
-    {
-        return exp2f(((high[i] - high[j]) + shift) + (low[i] - low[j]));
-    }
-    __device__ __forceinline__ float from_entry(int i, float shift) const { return exp2f((high[i] + shift) + low[i]); }
+    __device__ __forceinline__ float decay(int i, int j, int shift = 0) const { return power2(whole[i] - whole[j] + shift, frac[i] - frac[j]); }
+    __device__ __forceinline__ float from_entry(int i, int shift) const { return power2(whole[i] + shift, frac[i]); }
 };
+
+// log2 of a decay (no less than 2^-120, or not finite): the exponent exactly, and a fraction of at most 1/2, which log2f
+// leaves 2^-25 off.  log2f of the whole would leave 1e-5 of a decay of 1e-35.
+__device__ __forceinline__ double log2_of(float a)
+{
+    const int bits = __float_as_int(a);
+    int n = (bits >> 23) - 127;
+    float m = __int_as_float((bits & 0x7fffff) | 0x3f800000);
+    if (n == 128) return (double)a;
+    if (m > 1.41421356f) {
+        m *= 0.5f;
+        ++n;
+    }
+    return (double)n + (double)log2f(m);
+}
 
 // The products that a decay's gradient sums up (M) are the size of the decay, down to 2^-120 of the gradients given, and
 // would leave fp32's range before the division by it.  A chunk with a decay under 2^-40 holds them 2^60 times larger (an
 // exact factor): 24 bits then down to given gradients of 2^-42 at a decay of 2^-120, and of 2^-62 where none is under
 // 2^-40, without bringing products of ordinary decays, up to 2^67, out of range at the other end.
 struct Lift {
-    float shift, up, down;
+    int shift;
+    float up, down;
 };
 // by whole warps
 __device__ __forceinline__ Lift lift_of(const Gates &g)
 {
     const int lane = threadIdx.x & 31;
     const bool strong = __any_sync(0xffffffffu, fminf(g.a[lane], g.a[lane + 32]) < 0x1p-40f);
-    return strong ? Lift{60.f, 0x1p60f, 0x1p-60f} : Lift{0.f, 1.f, 1.f};
+    return strong ? Lift{60, 0x1p60f, 0x1p-60f} : Lift{0, 1.f, 1.f};
 }
 
 // Workspace of one (direction, head, chunk), in bytes.  Tiles are row-major with the 16-byte pieces of a

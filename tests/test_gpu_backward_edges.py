@@ -50,3 +50,27 @@ def test_gradient_of_a_strong_decay_at_any_scale(dtype, dk, power, bidi):
     for t in (70, 100, 130):
         e = ref.rel(got[4][:, :, t].cpu(), want[4][:, :, t])
         assert e <= 1e-5, f"ddecay at token {t}: rel-L2 {e:.3e}"
+
+
+@pytest.mark.parametrize("dtype,dk,dv", [("fp32", 32, 32), ("bf16", 64, 32), ("bf16", 128, 64)])
+@pytest.mark.parametrize("T,low,high", [(1, 1e-30, 1e-30), (3, 1e-12, 1.1e-12), (64, 0.25, 0.35), (64, 0.99, 1.0)])
+def test_products_of_strong_decays(dtype, dk, dv, T, low, high):
+    """With keys of zero the state only decays, so dstate_in = prod a dstate and da_t = prod_{s != t} a_s <dstate, state>
+    value by value.  A token's log2 is off by 2^-25 at most (its fraction's last place), 2^x by 2^-22 of itself for an
+    exponent split exactly, and a few roundings follow: T 2^-25 + 2^-20 together.  A result under 2^-126 (1e-36 times an
+    entry of dstate near 0) has fp32's spacing there, 2^-149, and no more bits: that much is added."""
+    a = make(1, 3, T, dk, dv, dtype, 5, False, True)
+    for x in (a[0], a[1], a[5]):
+        x.zero_()
+    g = torch.Generator().manual_seed(T)
+    a[4] = low + (high - low) * torch.rand(1, 3, T, generator=g)
+    a[6] = torch.zeros_like(a[6])
+    a[6][..., 3, 5] = 1.0                                # one entry: the inner product is one product
+    a[7] = torch.randn(a[7].shape, generator=g)
+    got = run(a, False)
+    prod = a[4].double().prod(-1)
+    tol = T * 2.0 ** -25 + 2.0 ** -20
+    want = [prod[..., None] / a[4].double() * a[7][..., 3, 5].double()[..., None], prod[..., None, None] * a[7].double()]
+    for name, x, y in zip(NAMES[4:], got[4:], want):
+        off = (((x.cpu().double() - y).abs() - 2.0 ** -149).clamp(min=0) / y.abs()).max()
+        assert off <= tol, f"{name}: {off:.3e} > {tol:.3e}"
