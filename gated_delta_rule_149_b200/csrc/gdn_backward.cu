@@ -26,8 +26,7 @@
 // Products run on the tensor cores with bf16 operands and fp32 sums, at fp32 grade: an fp32 operand is three bf16
 // terms, x = h + m + l (24 bits of significand), and of the products of terms those of total order under three are
 // taken; a bf16 input is one term and exact.  Two terms would halve the products and leave 3e-6 (rel-L2) in the fp32
-// gradients where three leave 2e-7; only the products with E and F, where their results (dQ, dK) are rounded to bf16,
-// take two.
+// gradients where three leave 2e-7.
 //
 // Kernels:
 // * prepare (a block per chunk and direction): brings K, Q, V, dO into scan order as term planes in the
@@ -913,7 +912,7 @@ template <int DK, int NI>
 struct GradSmem {
     using U = Unit<DK, NI>;
     static constexpr bool kStage = NI == 1;                    // room for the next step's fp32 tiles
-    static constexpr int NE = NI == 1 ? 2 : 3;                 // terms of E and F (results of NI = 1 are bf16)
+    static constexpr int NE = 3;                               // terms of E and S
     static constexpr int kOTiles = NI == 1 ? 4 : 1;            // dO: every slice, or the step's
     static constexpr int kState = kStep * DK * 2, kVal = kStep * kC * 2;
     struct Walk {                                              // term planes of the step's H0, dH1, U, Y: rows dv

@@ -45,13 +45,15 @@ using U1 = bwd::Unit<128, 1>;
 enum { cHD = 0, cHY = 64, cDU = 128, cPP = 192, cXX = 256, cKK = 320, cQK = 384, cEK = cPP, cSK = cXX, kCols = 512 };
 
 struct Smem {
-    // Offsets from a 1024-byte boundary.  Behind the walk over dv the buffers hold what two threads of PP, XX, KK
-    // and QK exchange (the place of H0 and dH1 of the first; F^T over PP's; KK and QK of half the tokens in the second,
-    // behind the terms of E^T and S), and then dQ and dK.  V collects dV.
+    // Offsets from a 1024-byte boundary.  Behind the walk over dv the first buffer holds what two threads of PP, XX, KK
+    // and QK exchange (the place of H0, dH1 and some of U; F^T over PP's; KK and QK of half the tokens) and the warps'
+    // parts of db (the rest of U), the second the terms of E^T and S (H0 and dH1); and then the first dQ and dK.  V
+    // collects dV.
     static constexpr int K = 0, Q = K + kKeys, O = Q + kKeys, V = O + 4 * 64 * 64, buf = V + kKeys, end = buf + 2 * kBuf;
-    static constexpr int dbw = buf + oU;       // the warps' parts of db
-    static constexpr int xP = buf, xX = xP + 64 * kLd * 4, E = buf + kBuf, S = E + 2 * kSq, xK = S + 2 * kSq, out = buf;
-    static_assert(xX + 64 * kLd * 4 <= buf + oU && xK + 2 * 64 * 32 * 4 <= buf + kBuf + oU, "the walk's zeros stay");
+    static constexpr int dbw = buf + oU + 2 * kVal;
+    static constexpr int xP = buf, xX = xP + 64 * kLd * 4, xK = xX + 64 * kLd * 4, E = buf + kBuf, S = E + 3 * kSq, out = buf;
+    static_assert(xK + 2 * 64 * 32 * 4 <= dbw && dbw + 16 * 64 * 4 <= buf + oZero && S + 3 * kSq <= buf + kBuf + oZero,
+                  "the walk's zeros stay");
     struct Small {
         Gates g;
         float db[64], da[64];                   // over the directions, by token
@@ -176,16 +178,16 @@ __device__ __forceinline__ void issue_step(uint32_t tmem, uint32_t base, int at,
     }
 }
 
-// EK = K^T E^T, SK = K^T S + Q^T E, of two terms of E and S
+// EK = K^T E^T, SK = K^T S + Q^T E, of three terms of E and S
 __device__ __forceinline__ void issue_tail(uint32_t tmem, uint32_t base)
 {
     const uint32_t k0 = desc_lo(base + Smem::K, 8192), q0 = desc_lo(base + Smem::Q, 8192);
     const uint32_t e0 = desc_lo(base + Smem::E, 16), s0 = desc_lo(base + Smem::S, 16);
 #pragma unroll
-    for (int x = 1; x >= 0; --x)
+    for (int x = 2; x >= 0; --x)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-            const uint32_t acc = x == 0 || k > 0, o = step_of(k * 2048), e = e0 + step_of(x * kSq);
+            const uint32_t acc = x < 2 || k > 0, o = step_of(k * 2048), e = e0 + step_of(x * kSq);
             mma(tmem + cEK, k0 + o, kDesc128, e + o, kDesc128, kIdMM, acc);
             mma(tmem + cSK, k0 + o, kDesc128, s0 + step_of(x * kSq) + o, kDesc128, kIdMM, acc);
             mma(tmem + cSK, q0 + o, kDesc128, e + step_of(k * 32), kDesc128, kIdMK, 1);
@@ -404,11 +406,11 @@ __device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint
                 pp[i] = x * lift.down;
             }
             {
-                uint32_t v[4][2];
+                uint32_t v[4][3];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) bwd::split2<2>(pp[2 * i], pp[2 * i + 1], v[i]);
+                for (int i = 0; i < 4; ++i) bwd::split2<3>(pp[2 * i], pp[2 * i + 1], v[i]);
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int x = 0; x < 3; ++x)
                     *reinterpret_cast<uint4 *>(sm + Smem::E + x * kSq + bwd::sw<128>(j, g8)) = make_uint4(v[0][x], v[1][x], v[2][x], v[3][x]);
             }
             // sums of M over this warp's i >= t for each of its t, then over its lanes j < t; its tokens' whole sum for each
@@ -428,13 +430,13 @@ __device__ __forceinline__ void workers(const BwdParams &p, Smem::Small &s, uint
             {                                                   // S = F + F^T
                 const int row = tid >> 3, c2 = tid & 7;
                 const float *f = reinterpret_cast<const float *>(sm + Smem::xP);
-                uint32_t v[4][2];
+                uint32_t v[4][3];
 #pragma unroll
                 for (int i = 0; i < 8; i += 2)
-                    bwd::split2<2>(f[row * kLd + 8 * c2 + i] + f[(8 * c2 + i) * kLd + row],
+                    bwd::split2<3>(f[row * kLd + 8 * c2 + i] + f[(8 * c2 + i) * kLd + row],
                                    f[row * kLd + 8 * c2 + i + 1] + f[(8 * c2 + i + 1) * kLd + row], v[i / 2]);
 #pragma unroll
-                for (int x = 0; x < 2; ++x)
+                for (int x = 0; x < 3; ++x)
                     *reinterpret_cast<uint4 *>(sm + Smem::S + x * kSq + bwd::sw<128>(row, c2)) = make_uint4(v[0][x], v[1][x], v[2][x], v[3][x]);
             }
             hand_over(&s.full[2]);                              // PP and XX are read: EK and SK may take their place

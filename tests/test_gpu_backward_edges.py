@@ -74,3 +74,27 @@ def test_products_of_strong_decays(dtype, dk, dv, T, low, high):
     for name, x, y in zip(NAMES[4:], got[4:], want):
         off = (((x.cpu().double() - y).abs() - 2.0 ** -149).clamp(min=0) / y.abs()).max()
         assert off <= tol, f"{name}: {off:.3e} > {tol:.3e}"
+
+
+@pytest.mark.parametrize("dk", [64, 128])
+def test_pair_products_keep_fp32_where_they_cancel(dk):
+    """Two tokens with opposite unit keys: dq_1 = (E_10 - E_11) k_0 = -(v_1 . do_1) k_0, where E_10 = do_1 . v_0 in [1, 2) has 24
+    bits (three parts of 8) and the difference is 1.5 * 2^-14.  The sums' truncation is at most 2^-23 of each of the
+    four products and three orders of terms, twice: 2^-20 covers it.  Pairs held in 16 bits would leave up to 2^-17."""
+    H, dv = 64, 64
+    a = make(1, H, 2, dk, dv, "bf16", 3, False, False)
+    q, k, v, beta, decay, do = a[:6]
+    for x in (k, v, do):
+        x.zero_()
+    beta.fill_(1.0)
+    decay.fill_(1.0)
+    k[:, :, 0, 0], k[:, :, 1, 0] = 1.0, -1.0
+    v[:, :, 0, :3] = (1 + torch.randint(0, 115, (1, H, 3), generator=torch.Generator().manual_seed(1)) / 128.0).bfloat16()
+    v[:, :, 1, 3] = 1.5
+    for c, power in enumerate((0, -8, -16, -14)):
+        do[:, :, 1, c] = 2.0 ** power
+    dq = run(a, False)[0].cpu().double()
+    want = torch.zeros_like(dq)
+    want[:, :, 1, 0] = -1.5 * 2.0 ** -14
+    off = (dq - want).abs().max()
+    assert off <= 2.0 ** -20 + 2.0 ** -9 * 1.5 * 2.0 ** -14, f"{off:.3e}"
