@@ -81,6 +81,9 @@ int rotary(bool back, const gdn_view *dq, const gdn_view *dk, const gdn_view *q,
     } else if (grid_h <= 0 || grid_w <= 0 || start < 0 || start > (1ll << 52)) {
         return fail(GDN_ERR_INVALID_ARG, "without positions, grid_h and grid_w must be positive and start in [0, 2^52] "
                     "(got %d, %d, %lld)", grid_h, grid_w, start);
+    } else if ((start + T - 1) / ((long long)grid_h * grid_w) > INT_MAX) {
+        return fail(GDN_ERR_INVALID_ARG, "the last token's frame, token %lld of frames of %d x %d, is beyond 2^31",
+                    start + T - 1, grid_h, grid_w);
     }
     const bool two = k || dk || yk;
     gdn::RotaryArgs a = {};

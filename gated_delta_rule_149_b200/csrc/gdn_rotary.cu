@@ -10,9 +10,11 @@
 //
 // One pass over the data, which bounds it: q and k are read in whatever strides the projection left them and
 // written in whatever strides the next operator takes.  The angles are formed in 64 bits as turns
-// (position * frequency / 2 pi), whose fraction alone goes to the 32-bit sine and cosine: a far position costs no
-// accuracy.  A block takes a tile of tokens, forms their sines and cosines once in shared memory, and all heads of
-// q and k use them; a thread keeps those of its eight pairs in registers over its heads.
+// (position * frequency / 2 pi), whose fraction alone goes to the 32-bit sine and cosine.  The turns are within 2^-50 of
+// themselves (the frequency and four roundings): nothing beside fp32 up to 2^24 radians, 2^-19 at 2^31, where positions end
+// (int32 ones, and by the check of the arguments those of a grid).  A block takes a tile of tokens, forms their sines and
+// cosines once in shared memory, and all heads of q and k use them; a thread keeps those of its eight pairs in
+// registers over its heads.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 

@@ -336,7 +336,8 @@ typedef struct gdn_view {
  * [B or 1][T][3]; pos_stride_b elements between batches, 0 to share one set), its
  * values, of any sign; with NULL, token t is number start + t of a sequence of
  * frames of grid_h x grid_w tokens, row by row (a streaming chunk gives the
- * number of tokens before it as start).
+ * number of tokens before it as start; no frame's number may pass 2^31 - 1).
+ * Angles are formed in 64 bits: a position p costs at most p 2^-50 radians, 2^-19 at 2^31.
  *
  * gdn_rotary_backward takes the gradients dq, dk of the outputs and, with
  * GDN_ROTARY_L2, the inputs q, k (else NULL), and writes the inputs' gradients.
@@ -345,7 +346,7 @@ typedef struct gdn_view {
  * boundaries, take a slower element-wise path.  Outputs must not overlap
  * anything.  No workspace.
  * Errors: GDN_ERR_INVALID_ARG for NULL data, sizes or strides out of range, axes
- * that do not sum to d, start < 0, theta <= 0, eps <= 0 with GDN_ROTARY_L2;
+ * that do not sum to d, start < 0 or frames beyond 2^31, theta <= 0, eps <= 0 with GDN_ROTARY_L2;
  * GDN_ERR_UNSUPPORTED for d > 256; GDN_ERR_MISALIGNED for data off its element
  * size.
  */

@@ -44,3 +44,14 @@ def test_gates_without_bounds(dtype):
     assert torch.isposinf(y[0]).all() and y[1:3].isnan().all() and (y[3] == 0).all()
     want = g[0, 0, 4:].double() * (1 + 1e-5) ** -0.5
     ref.close(y[4:], want, dtype, FINE * want)
+
+
+@pytest.mark.parametrize("grid,start", [((1, 1), 2 ** 31 - 40), ((64, 128), 2 ** 40), ((1 << 12, 1 << 13), 2 ** 52 - 2 ** 25)])
+def test_rotary_far_positions(grid, start):
+    """A grid's positions up to the largest that int32 positions have, and token numbers far beyond: three roundings to 53
+    bits and the power's own error leave 3 * 2^-52 of the angle, 2^-19 at 2^31 (see the neighbouring int32 test), and fp32's part."""
+    T, d = 40, 96
+    q = normal(1, 2, T, d, seed=3)
+    y = gdn_rotary(q, axes=(32, 32, 32), grid=grid, start=start)
+    want = ref.rotary(q.cpu(), (32, 32, 32), 10000.0, False, ref.grid_positions(T, grid, start), False, 1e-6)
+    ref.close(y.cpu(), want, FP32, 4 * FINE * norms(q).cpu())
