@@ -182,6 +182,8 @@ def _run(device, stream, call):
     that stream's.  The usual case, the current device and its current stream, switches nothing."""
     if stream is None and torch.cuda.current_device() == device.index:
         return call(torch._C._cuda_getCurrentRawStream(device.index))
+    if stream is not None and stream.device != device:
+        raise ValueError(f"stream: expected one of {device}, got one of {stream.device}")
     with torch.cuda.device(device), torch.cuda.stream(stream):
         return call(torch._C._cuda_getCurrentRawStream(device.index))
 

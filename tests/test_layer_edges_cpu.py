@@ -12,3 +12,17 @@ def test_rotary_refuses_frames_beyond_int32(lib, grid, start, code):
     got = rot(lib, gh=grid[0], gw=grid[1], start=start, q=view(0))
     assert got == -1 and (b"frame" in lib.gdn_last_error()) == (code != 0)
     assert code or b"q must be" in lib.gdn_last_error()
+
+
+def test_a_stream_of_another_device_is_refused():
+    """torch.cuda.stream makes the stream's device current: the kernels would run there, on pointers of the tensors' device."""
+    import types
+
+    import torch
+    from gated_delta_rule_149_b200.gdn import _run
+
+    def call(handle):
+        raise AssertionError("called")
+
+    with pytest.raises(ValueError, match="stream"):
+        _run(torch.device("cuda", 0), types.SimpleNamespace(device=torch.device("cuda", 1)), call)
