@@ -44,6 +44,9 @@
 #include "gdn_chunk_common.cuh"
 
 namespace gdn {
+
+extern int g_stall_chunk;      // gdn_debug_stall
+
 namespace {
 
 using namespace bwd;
@@ -346,10 +349,11 @@ __global__ void __launch_bounds__(kPrepThreads, NI == 1 ? 4 : 1) bwd_prepare_ker
 struct Loads {
     uint64_t bar[2];
     int abort;
-    __device__ __forceinline__ void init()
+    // stall (testing): the first stage waits for an arrival more than it gets
+    __device__ __forceinline__ void init(bool stall)
     {
         if (threadIdx.x == 0) {
-            mbar_init(&bar[0], 1);
+            mbar_init(&bar[0], stall ? 2 : 1);
             mbar_init(&bar[1], 1);
             abort = 0;
             fence_mbar_init();
@@ -364,7 +368,9 @@ struct Loads {
         bulk_load(to, unit, head, &bar[b]);
         bulk_load(to + head, tile, bytes, &bar[b]);
     }
-    __device__ __forceinline__ bool wait(int b, uint32_t parity, int *err) { return wait_bar(&bar[b], parity, &abort, err, 128); }
+    // whether the stage is there; when a wait ran out, not before its copies have landed (or a second limit has passed): the
+    // block leaves then
+    __device__ __forceinline__ bool wait(int b, uint32_t parity, int *err) { return wait_copies(&bar[b], parity, &abort, err, 128); }
 };
 
 // bytes of one stage: the unit's tiles from its start (forward: gates, N, K; backward: all) and V or dO
@@ -489,7 +495,7 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
         }
     };
 
-    loads.init();
+    loads.init(p.stall && head == 0);
     if (S::buffers == 2) fetch(0);
     for (int step = 0; step < p.nc; ++step) {
         const int c = (dir ^ WALK) ? p.nc - 1 - step : step;
@@ -711,7 +717,7 @@ __device__ __forceinline__ void chain_narrow(const BwdParams &p, int dir, unsign
         }
     };
 
-    loads.init();
+    loads.init(p.stall && head == 0);
     if (S::buffers == 2) fetch(0);
     for (int step = 0; step < p.nc; ++step) {
         const int c = (dir ^ WALK) ? p.nc - 1 - step : step;
@@ -1360,6 +1366,7 @@ cudaError_t launch_backward(const BwdArgs &a, cudaStream_t stream)
     p.dq = a.dq; p.dk_ = a.dk; p.dv_ = a.dv; p.dbeta = a.dbeta; p.ddecay = a.ddecay; p.dstate_in = a.dstate_in;
     p.BH = a.f.B * a.f.H; p.T = a.f.T; p.nc = (a.f.T + bwd::kC - 1) / bwd::kC; p.dk = a.f.dk; p.dv = a.f.dv;
     p.dirs = a.f.bidi ? 2 : 1;
+    p.stall = g_stall_chunk >= 0;
     if (a.f.fp32) return p.dk <= 64 ? run<64, 3, float>(p, stream) : run<128, 3, float>(p, stream);
     return p.dk <= 64 ? run<64, 1, __nv_bfloat16>(p, stream) : run<128, 1, __nv_bfloat16>(p, stream);
 }

@@ -107,6 +107,7 @@ struct BwdParams {
     int head0, heads;          // the heads [head0, head0 + heads) of B*H
     int BH, T, nc, dk, dv, dirs, slices;
     int *err;                  // the device error word of bounded waits
+    int stall;                 // testing: the first waits of head 0's walks and of the first chunk's gradients run out
 };
 
 // A chunk of one scan: its tokens in scan order.  Chunks are tiles [64 c, 64 c + n) of the sequence for

@@ -59,6 +59,7 @@ struct Smem {
         float db[64], da[64];                   // over the directions, by token
         float m0[4][64], m1[4][64], col[2][64], whole[8][64], hh[16];
         uint64_t full[3], done[3];              // a buffer's operands are there, its products are done; the last products'
+        uint64_t drain;                         // behind a wait that ran out: every product issued is done
         uint32_t tmem;
         int abort;
     };
@@ -550,9 +551,10 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_grad_tc_kernel(const __grid_c
     if (warp == 0) tmem_alloc(&s.tmem, kCols);
     if (tid == 0) {
         for (int i = 0; i < 3; ++i) {
-            mbar_init(&s.full[i], kWorkers / 32);
+            mbar_init(&s.full[i], kWorkers / 32 + (p.stall && p.head0 + blockIdx.x + i == 0));
             mbar_init(&s.done[i], 1);
         }
+        mbar_init(&s.drain, 1);
         s.abort = 0;
         fence_mbar_init();
     }
@@ -568,6 +570,14 @@ __global__ void __launch_bounds__(kThreads, 1) bwd_grad_tc_kernel(const __grid_c
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (*static_cast<volatile int *>(&s.abort)) {
+        // products still in flight read shared memory and write tensor memory: none may outlive the block
+        if (tid == kWorkers) {
+            mma_commit(&s.drain);
+            drain_copies(&s.drain, 0);
+        }
+        __syncthreads();
+    }
     if (warp == 0) {
         tmem_relinquish();
         tmem_dealloc(tmem, kCols);

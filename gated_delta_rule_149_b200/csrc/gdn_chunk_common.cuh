@@ -71,6 +71,35 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatil
     return wait_bar_slow(bar, parity, abort_flag, err, code);
 }
 
+// Waits (bounded) for copies still in flight on a transaction barrier after an abort.
+__device__ __forceinline__ void drain_copies(uint64_t *bar, uint32_t parity)
+{
+    const unsigned long long t0 = globaltimer();
+    while (!mbar_try_wait(bar, parity) && globaltimer() - t0 < 200000000ull) {}
+}
+
+// wait_bar for copies on their way into the CTA's own shared memory: when the wait ran out, it returns only after they have
+// landed (bounded again), so that the CTA may leave.
+__device__ __noinline__ bool wait_copies_slow(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err, int code)
+{
+    const unsigned long long t0 = globaltimer();
+    for (uint32_t it = 0; it < (1u << 30); ++it) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag || ((it & 255) == 255 && globaltimer() - t0 > g_wait_limit_ns)) break;
+    }
+    if (!*abort_flag) {
+        atomicOr(err, code);
+        *abort_flag = 1;
+    }
+    drain_copies(bar, parity);
+    return false;
+}
+__device__ __forceinline__ bool wait_copies(uint64_t *bar, uint32_t parity, volatile int *abort_flag, int *err, int code)
+{
+    if (mbar_try_wait(bar, parity)) return true;
+    return wait_copies_slow(bar, parity, abort_flag, err, code);
+}
+
 __device__ __forceinline__ void st_release_cta(int *addr, int v)
 {
     asm volatile("st.release.cta.shared.b32 [%0], %1;" ::"r"(smem_u32(addr)), "r"(v) : "memory");

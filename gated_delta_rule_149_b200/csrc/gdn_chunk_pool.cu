@@ -251,13 +251,6 @@ __device__ __forceinline__ void drain_mmas(Bars &B)
     while (!mbar_try_wait(&B.drain, 0) && globaltimer() - t0 < kWaitLimitNs) {}
 }
 
-// Waits (bounded) for copies still in flight on a transaction barrier after an abort.
-__device__ __forceinline__ void drain_copies(uint64_t *bar, uint32_t parity)
-{
-    const unsigned long long t0 = globaltimer();
-    while (!mbar_try_wait(bar, parity) && globaltimer() - t0 < 200000000ull) {}
-}
-
 __device__ __forceinline__ void st_release_gpu(int *addr, int v)
 {
     asm volatile("st.release.gpu.global.b32 [%0], %1;" ::"l"(addr), "r"(v) : "memory");

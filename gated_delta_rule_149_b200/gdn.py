@@ -465,7 +465,8 @@ def debug_ring(buf):
 def debug_stall(chunk):
     """Test hook: chunk >= 0 makes scan 0's state chain of the pooled kernel wait
     for that chunk's operands with a target nothing reaches, so the wait runs
-    out and the call ends with a device timeout status; -1 turns it off."""
+    out and the call ends with a device timeout status; -1 turns it off.  The same
+    for the first wait of head 0's walks in gdn_backward and of its chunk gradients on tcgen05."""
     load_library().gdn_debug_stall(int(chunk))
 
 

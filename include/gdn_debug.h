@@ -47,8 +47,9 @@ void gdn_debug_profile(long long *device_buffer);
  * gdn_debug_stall -- chunk c >= 0 makes scan 0's state chain in the pooled
  * kernel wait for chunk c's operands with a target that nothing reaches, so
  * that the wait runs out, the kernel records GDN_ERR_DEVICE_TIMEOUT in the
- * device error word and returns; -1 (default) turns it off.  Combine with
- * gdn_debug_wait_limit to keep the run short.
+ * device error word and returns; -1 (default) turns it off.  In gdn_backward any
+ * c >= 0 does the same to the first wait of head 0's walks, and of the first
+ * chunk's gradients where they run on tcgen05 (bf16, dk of 96 or 128).  Combine with gdn_debug_wait_limit to keep the run short.
  */
 void gdn_debug_stall(int chunk);
 
@@ -62,8 +63,8 @@ void gdn_debug_plain_launch(int on);
 
 /*
  * gdn_debug_wait_limit -- the limit, in nanoseconds, of every bounded wait in
- * the chunkwise kernels on the current device; 0 restores the default (4 s).
- * Synchronous.  Returns GDN_OK or GDN_ERR_CUDA.
+ * the chunkwise kernels, gdn_backward's among them, on the current device; 0
+ * restores the default (4 s).  Synchronous.  Returns GDN_OK or GDN_ERR_CUDA.
  */
 int gdn_debug_wait_limit(unsigned long long ns);
 

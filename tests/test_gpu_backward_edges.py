@@ -1,11 +1,14 @@
 """gdn_backward where gates, scales and values are at their ends, and where a block takes more than one chunk.
 
 Tolerances as in test_gpu_backward.py (rel-L2 1e-5, and 2^-8 for outputs of bf16 type) unless a test derives its own."""
+import time
+
 import pytest
 import torch
 
 import layer_reference as ref
-from gated_delta_rule_149_b200 import gdn_backward
+from gated_delta_rule_149_b200 import gdn, gdn_backward, gdn_device_status
+from gated_delta_rule_149_b200.gdn import GDNError
 from test_gpu_backward import NAMES, make, run
 
 pytestmark = pytest.mark.gpu
@@ -98,3 +101,35 @@ def test_pair_products_keep_fp32_where_they_cancel(dk):
     want[:, :, 1, 0] = -1.5 * 2.0 ** -14
     off = (dq - want).abs().max()
     assert off <= 2.0 ** -20 + 2.0 ** -9 * 1.5 * 2.0 ** -14, f"{off:.3e}"
+
+
+@pytest.mark.parametrize("dtype,dk,dv,H,T,bidi,code", [
+    ("bf16", 128, 128, 2, 300, False, 192), ("bf16", 128, 32, 2, 300, True, 192), ("bf16", 128, 64, 100, 130, True, 192),
+    ("fp32", 64, 64, 2, 200, True, 128), ("fp32", 128, 96, 80, 130, False, 128)])
+def test_waits_run_out_and_the_next_call_is_correct(dtype, dk, dv, H, T, bidi, code):
+    """Head 0's walks wait for what never comes (128) and so do, on tcgen05, its first chunk's gradients (64): the waits run out
+    after 20 ms, the blocks let their copies and products end and leave, the status says so once, and a clean call is right.
+    With few heads and with many (both forms of the walks), one step of dv and several."""
+    a = make(1, H, T, dk, dv, dtype, 7, bidi, True, shift=1.0)
+    dev = [x.cuda() for x in a]
+    gdn_device_status()
+    gdn.debug_wait_limit(20_000_000)
+    gdn.debug_stall(1)
+    try:
+        start = time.perf_counter()
+        gdn_backward(*dev, bidi=bidi)
+        with pytest.raises(GDNError) as err:
+            gdn_device_status()
+        took = time.perf_counter() - start
+    finally:
+        gdn.debug_stall(-1)
+        gdn.debug_wait_limit(0)
+    assert err.value.code == -5 and f"code {code})" in str(err.value)
+    assert took < 10.0
+    gdn_device_status()
+    got = gdn_backward(*dev, bidi=bidi)
+    gdn_device_status()
+    part = [x[:, :2] for x in dev[:7]] + [dev[7][..., :2, :, :]]
+    for name, x, y in zip(NAMES, got, ref.recurrence_gradients(*part, bidi)):
+        tol = 1e-5 + (2.0 ** -8 if x.dtype == torch.bfloat16 else 0.0)
+        assert ref.rel(x[:, :2], y) <= tol, name
