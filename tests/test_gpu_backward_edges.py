@@ -133,3 +133,21 @@ def test_waits_run_out_and_the_next_call_is_correct(dtype, dk, dv, H, T, bidi, c
     for name, x, y in zip(NAMES, got, ref.recurrence_gradients(*part, bidi)):
         tol = 1e-5 + (2.0 ** -8 if x.dtype == torch.bfloat16 else 0.0)
         assert ref.rel(x[:, :2], y) <= tol, name
+
+
+@pytest.mark.parametrize("dk,dv,H,T,dtype,bidi", [
+    (128, 32, 160, 130, "bf16", True), (128, 64, 160, 130, "bf16", True), (96, 96, 160, 130, "bf16", True),
+    (128, 128, 160, 130, "bf16", True), (128, 128, 160, 200, "bf16", False), (128, 96, 150, 65, "bf16", False),
+    (64, 32, 160, 70, "fp32", True), (128, 96, 80, 70, "fp32", True)])
+def test_more_chunks_than_sms(dk, dv, H, T, dtype, bidi):
+    """The chunk gradients' blocks take two to four chunks each, in one and in both directions, with one to four steps of
+    32 columns; the chains' blocks of 64 columns have an odd number of 32 to fill.  The definition in 64 bits on the GPU."""
+    a = [None if x is None else x.cuda() for x in make(1, H, T, dk, dv, dtype, dk + dv + T, bidi, True, shift=1.0)]
+    got = gdn_backward(*a, bidi=bidi)
+    for h in range(0, H, 32):
+        part = [x[:, h:h + 32] for x in a[:7]] + [a[7][..., h:h + 32, :, :]]
+        want = ref.recurrence_gradients(*part, bidi)
+        for name, x, y in zip(NAMES, got, want):
+            tol = 1e-5 + (2.0 ** -8 if x.dtype == torch.bfloat16 else 0.0)
+            e = ref.rel(x[:, h:h + 32], y)
+            assert e <= tol, f"{name}, heads {h} ..: rel-L2 {e:.3e}"

@@ -55,3 +55,52 @@ def test_rotary_far_positions(grid, start):
     y = gdn_rotary(q, axes=(32, 32, 32), grid=grid, start=start)
     want = ref.rotary(q.cpu(), (32, 32, 32), 10000.0, False, ref.grid_positions(T, grid, start), False, 1e-6)
     ref.close(y.cpu(), want, FP32, 4 * FINE * norms(q).cpu())
+
+
+def test_rotary_repeated_positions_turn_equal_rows_equally():
+    B, H, T, d = 2, 3, 6, 64
+    pos = torch.randint(-10 ** 6, 10 ** 6, (B, T, 3), generator=torch.Generator().manual_seed(5), dtype=torch.int64).to(torch.int32)
+    pos[:, 1] = pos[:, 0]
+    q = normal(B, H, T, d, seed=4)
+    q[:, :, 1] = q[:, :, 0]
+    y = gdn_rotary(q, axes=(24, 20, 20), positions=pos.cuda(), l2norm=True)
+    assert torch.equal(y[:, :, 0], y[:, :, 1])
+    assert not torch.equal(y[:, :, 0], y[:, :, 2])
+
+
+def test_outputs_behind_element_2_to_31():
+    """The C entry points with outputs whose second batch starts behind element 2^31 of a buffer: written there and nowhere
+    near; read there by the gradients."""
+    lib = load_library()
+    B, H, T, d, far = 2, 2, 5, 128, 2 ** 31
+    room = torch.full((far + 2 ** 14,), 7.0, dtype=BF16, device="cuda")
+    big = room.as_strided((B, H, T, d), (far, T * d + 8, d, 1), storage_offset=16)
+    to = View(big.data_ptr(), far, T * d + 8, d)
+    mine = torch.zeros_like(room, dtype=torch.bool)
+    mine.as_strided((B, H, T, d), (far, T * d + 8, d, 1), storage_offset=16).fill_(True)
+    x, g, w = normal(B, H, T, d, dtype=BF16, seed=1), normal(B, H, T, d, dtype=BF16, seed=2), normal(d, seed=3)
+    frm, gate = (View(t.data_ptr(), H * T * d, T * d, d) for t in (x, g))
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+    def wrote(want):
+        assert torch.equal(big, want)
+        for a in range(0, room.numel(), 2 ** 29):          # what lies between the rows is as it was
+            assert bool(((room[a:a + 2 ** 29] == 7.0) | mine[a:a + 2 ** 29]).all())
+
+    how = (None, 0, B, H, T, d, 44, 42, 42, 2, 2, 0, 1e4, 1e-6, 32, stream)
+    assert lib.gdn_rotary(frm, None, to, None, *how) == 0
+    wrote(gdn_rotary(x, axes=(44, 42, 42), grid=(2, 2), l2norm=True))
+    big.fill_(0)
+    assert lib.gdn_gated_norm(frm, gate, w.data_ptr(), 0, to, B, H, T, d, 1e-5, 0, stream) == 0
+    wrote(gdn_gated_norm(x, g, w).view(B, T, H, d).transpose(1, 2))
+    dy = normal(B, T, H * d, dtype=BF16, seed=4)
+    vdy = View(dy.data_ptr(), T * H * d, d, H * d)
+    do, dg, dw = torch.empty_like(x), torch.empty_like(x), torch.empty_like(w)
+    vdo, vdg = (View(t.data_ptr(), H * T * d, T * d, d) for t in (do, dg))
+    want = gdn_gated_norm_backward(dy, x, g, w)
+    big.copy_(x)                                           # read behind 2^31
+    assert lib.gdn_gated_norm_backward(vdy, to, gate, w.data_ptr(), 0, vdo, vdg, dw.data_ptr(), B, H, T, d, 1e-5, 0, stream) == 0
+    assert torch.equal(do, want[0]) and torch.equal(dg, want[1]) and torch.equal(dw, want[2])
+    big.fill_(0)                                           # written behind 2^31
+    assert lib.gdn_gated_norm_backward(vdy, frm, gate, w.data_ptr(), 0, to, vdg, dw.data_ptr(), B, H, T, d, 1e-5, 0, stream) == 0
+    wrote(want[0])
