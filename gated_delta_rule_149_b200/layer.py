@@ -226,17 +226,19 @@ class LayerSaved(NamedTuple):
 
 def gdn_layer_forward(q, k, v, beta, decay, gate=None, weight=None, state_in=None, *, axes, grid=None, start=0,
                       positions=None, theta=10000.0, half=False, l2norm=True, eps=1e-6, norm_eps=1e-5, bidi=False,
-                      stream=None):
+                      recurrent=False, stream=None):
     """A GDN layer between its projections: gdn_rotary on q and k, gdn_forward, gdn_gated_norm.
 
     q, k, gate: [B,H,T,d] views of the projections; v contiguous [B,H,T,dv]; beta,
     decay, state_in as gdn_forward; the keywords as gdn_rotary (l2norm=True here:
-    the recurrence wants unit keys), norm_eps for the read-out's norm.  Returns
-    y [B,T,H*dv], the final state, and what gdn_layer_backward needs.
+    the recurrence wants unit keys), norm_eps for the read-out's norm, recurrent as
+    gdn_forward (bf16 with other sizes than dk = 128, dv = 64 or 128 needs it).
+    Returns y [B,T,H*dv], the final state, and what gdn_layer_backward needs.
     """
     how = dict(axes=axes, grid=grid, start=start, positions=positions, theta=theta, half=half, l2norm=l2norm, eps=eps)
     qr, kr = gdn_rotary(q, k, **how, stream=stream)
-    o, state = _run(q.device, stream, lambda _: gdn_forward(qr, kr, v, beta, decay, state_in, bidi=bidi, stream=stream))
+    o, state = _run(q.device, stream, lambda _: gdn_forward(qr, kr, v, beta, decay, state_in, bidi=bidi, recurrent=recurrent,
+                                                              stream=stream))
     y = gdn_gated_norm(o, gate, weight, eps=norm_eps, stream=stream)
     return y, state, LayerSaved(q, k, qr, kr, v, beta, decay, state_in, o, gate, weight, bidi, norm_eps, how)
 

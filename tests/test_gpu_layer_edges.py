@@ -7,8 +7,9 @@ import pytest
 import torch
 
 import layer_reference as ref
-from gated_delta_rule_149_b200 import gdn_gated_norm, gdn_gated_norm_backward, gdn_rotary, load_library
-from gated_delta_rule_149_b200.gdn import View
+from gated_delta_rule_149_b200 import (gdn_backward, gdn_forward, gdn_gated_norm, gdn_gated_norm_backward, gdn_layer_backward,
+                                       gdn_layer_forward, gdn_rotary, gdn_rotary_backward, load_library)
+from gated_delta_rule_149_b200.gdn import GDNError, View
 from test_gpu_layer_ops import BF16, FINE, FP32, norms, normal
 
 pytestmark = pytest.mark.gpu
@@ -104,3 +105,29 @@ def test_outputs_behind_element_2_to_31():
     big.fill_(0)                                           # written behind 2^31
     assert lib.gdn_gated_norm_backward(vdy, frm, gate, w.data_ptr(), 0, to, vdg, dw.data_ptr(), B, H, T, d, 1e-5, 0, stream) == 0
     wrote(want[0])
+
+
+@pytest.mark.parametrize("dk,dv", [(64, 32), (96, 96)])
+def test_layer_at_sizes_of_the_recurrent_form(dk, dv):
+    """bf16 at sizes that gdn_forward takes in its recurrent form and gdn_backward in its only one: the layer is the chain of
+    its calls, forward and back."""
+    B, H, T = 1, 3, 70
+    q, k = (normal(B, T, H, dk, dtype=BF16, seed=i).transpose(1, 2) for i in (1, 2))
+    v, gate = normal(B, H, T, dv, dtype=BF16, seed=3), normal(B, T, H, dv, dtype=BF16, seed=4).transpose(1, 2)
+    beta, decay = torch.sigmoid(normal(B, H, T, seed=5)), torch.sigmoid(2 + normal(B, H, T, seed=6))
+    w = 1 + 0.1 * normal(dv, seed=7)
+    how = dict(axes=(dk - 32, 16, 16), grid=(4, 5))
+    with pytest.raises(GDNError):
+        gdn_layer_forward(q, k, v, beta, decay, gate, w, **how)
+    y, state, saved = gdn_layer_forward(q, k, v, beta, decay, gate, w, recurrent=True, **how)
+    qr, kr = gdn_rotary(q, k, l2norm=True, **how)
+    o, st = gdn_forward(qr, kr, v, beta, decay, recurrent=True)
+    assert torch.equal(st, state) and torch.equal(y, gdn_gated_norm(o, gate, w))
+    dy = normal(B, T, H * dv, dtype=BF16, seed=8)
+    got = gdn_layer_backward(dy, saved)
+    do, dg, dw = gdn_gated_norm_backward(dy, o, gate, w)
+    dq, dk_, dv_, db, da, _ = gdn_backward(qr, kr, v, beta, decay, do)
+    dq, dk_ = gdn_rotary_backward(dq, dk_, q, k, l2norm=True, **how)
+    for name, x in dict(q=dq, k=dk_, v=dv_, beta=db, decay=da, gate=dg, weight=dw).items():
+        assert torch.equal(got[name], x), name
+    assert got["state_in"] is None
