@@ -639,7 +639,7 @@ __device__ __forceinline__ void chain(const BwdParams &p, int dir, unsigned char
 // counts.  A warp holds a quarter of dk of H^T.  Its partial H^T K^T goes to the others by tokens: warp q adds up tokens
 // 16 q .. 16 q + 15, multiplies them into its part of the triangular product, whose sums by tokens meet the same way,
 // and shares the finished W (or Z) of its tokens as left operands; nothing but the shared operands' loads is done twice.
-// (480p chunk, 16 heads of 74 chunks, dk = dv = 128, bf16: 3.7 us a chunk, 4.7 with pairs of warps.)
+// (480p chunk, 16 heads of 74 chunks, dk = dv = 128, bf16: 3.8 us a chunk, 4.7 with pairs of warps.)
 template <int DK, int NI, typename T, int WALK>
 struct StageNarrow {
     using U = Unit<DK, NI>;
