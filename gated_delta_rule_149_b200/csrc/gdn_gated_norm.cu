@@ -175,7 +175,7 @@ __global__ void __launch_bounds__(kThreads, BACK ? 4 : 6) gated_norm_kernel(cons
         if (!BACK) {
 #pragma unroll
             for (int i = 0; i < kPer; ++i) {
-                x[i] *= r * w[i];
+                x[i] = x[i] * r * w[i];
                 if (GATE) x[i] *= g[i] * sigmoid<T>(g[i]);
             }
             if (act) store<VEC, LPR>(y, l, p.dv, x);
