@@ -14,7 +14,7 @@
 // chunks, dv = 128: 170 us, where mma.sync tiles took 280; the tensor core is busy for a third of that, the rest is the
 // latency of loads, splitting and epilogue with sixteen warps of 96 registers.)  Products of terms are those of order
 // i + j < 3, the small ones first in each step.  The tensor core truncates its fp32 sums, and a result's run over all of dv here,
-// up to 48 products: 3 - 6e-7 (rel-L2) in the gradient of the decay, where the other kernel, which adds every few products by a
+// up to 48 products: 3e-7 to 1e-6 (rel-L2) in the gradient of the decay, where the other kernel, which adds every few products by a
 // rounded addition, leaves 2e-7 and elementary fp32 operations 2 - 3e-7.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -296,8 +296,8 @@ int gdn_forward_fp8(const void *q8, const void *k8, const void *v8,
  * unless NULL.  Nothing of the forward call is needed but its inputs: the states
  * are recomputed.  All arithmetic is of fp32 grade in both dtypes, whatever the
  * precision of the forward kernel that ran: fp32 operands in 24 bits, sums in fp32,
- * some of them truncated instead of rounded (at 1024 tokens dbeta and dstate_in are
- * 1 - 2e-7 off, ddecay 1 - 6e-7, rel-L2).
+ * some of them truncated instead of rounded (dbeta and dstate_in are 1 - 3e-7 off,
+ * ddecay 1e-7 to 1e-6, rel-L2).
  *
  * dk, dv: multiples of 32, <= 128, for both dtypes.  beta may be 0.  A decay below
  * 2^-120 acts as 2^-120 and has the gradient of that value (full precision for
